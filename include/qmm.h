@@ -355,6 +355,94 @@ qmm_status qmm_gather_qmm_static(const void *x, int64_t x_batch, int64_t M, int6
                                  const char *mode, int sorted_indices, void *y, void *stream);
 
 /*
+ * Mixture-of-experts layers: qmm_moe_route chooses each token's experts from
+ * the router's logits, qmm_moe_experts computes the chosen experts' gated
+ * feed-forward products on 4-bit stacked weights and adds them up.  The
+ * documents this library follows stop at gather_qmm; these two are what a
+ * model runs around it, without a host step between them.
+ *
+ * qmm_moe_route -- for each of T tokens the top_k experts and their weights.
+ *   logits   in : [T, E] in `dtype` (QMM_F32, QMM_BF16 or QMM_F16), aligned to
+ *                 its element size
+ *   bias     in : [E] fp32 or NULL: added to the scores to choose experts, not
+ *                 to weigh them
+ *   indices  out: [T, top_k] int32, the best expert first
+ *   weights  out: [T, top_k] fp32
+ * Scores s: QMM_SCORE_SOFTMAX, softmax of the token's logits; QMM_SCORE_SIGMOID,
+ *   sigmoid of each.  Experts are ordered by s + bias, or by the logit when
+ *   bias is NULL (the same order, without its rounding); equal keys go to the
+ *   lower index.  The order is the one of exact arithmetic on the given
+ *   logits and bias up to fp64 rounding, whatever the dtype.
+ * Groups: the experts form n_groups groups of E / n_groups neighbours
+ *   (n_groups divides E, at most 32).  A group's score is the sum of its
+ *   group_top (1 or 2) largest s + bias; only the experts of the topk_groups
+ *   best groups can be chosen (equal scores: the lower group).  n_groups = 1
+ *   for no groups.
+ * Weights: the chosen experts' s (no bias), divided by their sum if
+ *   renormalize, times scale (finite).
+ * Masked experts: a logit of -inf (score 0) or a bias of -inf ranks below every
+ *   finite key.  A token whose logits are all -inf has scores 0: it gets the
+ *   lowest indices and weights 0, and so do chosen experts whose sum is 0.
+ *   Softmax of logits that hold +inf is shared by those.  A NaN logit ranks
+ *   below everything and makes the token's weights NaN.
+ * Limits: 1 <= E <= 1024, 1 <= top_k <= min(32, topk_groups * E / n_groups).
+ *   T == 0 is a no-op.
+ */
+typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_score;
+qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t T, int64_t E,
+                         const float *bias, qmm_score score, int64_t n_groups,
+                         int64_t topk_groups, int group_top, int64_t top_k, int renormalize,
+                         double scale, int32_t *indices, float *weights, void *stream);
+
+/*
+ * qmm_moe_experts -- the experts' gated feed-forward layer:
+ *   h[t, j] = act(x[t] @ Wg[e]^T) * (x[t] @ Wu[e]^T),   e = indices[t, j]
+ *   y[t]    = sum over j of weights[t, j] * (h[t, j] @ Wd[e]^T)
+ *   x [T, K], y [T, N] in `dtype` (QMM_BF16 or QMM_F16); indices [T, top_k]
+ *   int32 and weights [T, top_k] fp32 (as qmm_moe_route writes them, 4-byte
+ *   aligned).  y must not overlap an input.
+ *   Weights stacked over experts and packed as by qmm_quantize with 4 bits:
+ *     gate_wq, up_wq [n_experts, I, K*4/32], scales [n_experts, I, K/group_size]
+ *     down_wq        [n_experts, N, I*4/32], scales [n_experts, N, I/group_size]
+ *   Modes: "mxfp4" and "nvfp4" (uint8 scales, biases NULL), and "affine" with
+ *   4 bits (scales and biases in `dtype`).
+ * act: QMM_ACT_SILU, v / (1 + e^-v); QMM_ACT_GELU_TANH, the tanh form of gelu.
+ * Slots: index -1 leaves a slot out (a padded token, an expert held
+ *   elsewhere); it adds nothing, whatever its weight.  Any other index outside
+ *   [0, n_experts) adds nothing either and a later qmm_device_status() reports
+ *   QMM_ERR_INDEX.  A token without a slot gets y = 0.  An expert may appear
+ *   twice for one token; both slots count.
+ * Rounding: sums are fp32 or exact integers, and y is rounded once.  With few
+ *   rows (and under QMM_PATH_GEMV) activations enter as 16-bit integers per 32
+ *   elements (error at most 2^-15 of their largest) and h stays fp32; with more
+ *   rows (and under QMM_PATH_GEMM) h is rounded to `dtype`, the tensor cores'
+ *   operand, and so is each weight of the "affine" mode and of "nvfp4" and
+ *   "mxfp4" where X * element is no `dtype` value (never for normal ones).
+ *   A slot's result is added in slot order: repeated calls return the same bits.
+ * workspace: device memory of qmm_moe_experts_workspace_size(...) bytes,
+ *   256-byte aligned; its contents need not be initialised and are not
+ *   preserved.  Two calls in flight at once must not share a workspace (two
+ *   captured graphs that may run at once need one each).  Too small or
+ *   misaligned: QMM_ERR_WORKSPACE.
+ * Limits: K and I multiples of 64 and of group_size, QMM_ERR_UNSUPPORTED for
+ *   other sizes of K and I, other bits or modes, QMM_F32, and more than 2^30
+ *   slots or stacked rows; n_experts <= 1024, top_k <= 32.  T == 0 or N == 0
+ *   is a no-op.
+ */
+typedef enum { QMM_ACT_SILU = 0, QMM_ACT_GELU_TANH = 1 } qmm_activation;
+size_t qmm_moe_experts_workspace_size(int64_t T, int64_t K, int64_t top_k, int64_t n_experts,
+                                      int64_t I, int64_t N, qmm_dtype dtype);
+qmm_status qmm_moe_experts(const void *x, int64_t T, int64_t K, qmm_dtype dtype,
+                           const int32_t *indices, const float *weights, int64_t top_k,
+                           const uint32_t *gate_wq, const void *gate_scales,
+                           const void *gate_biases, const uint32_t *up_wq,
+                           const void *up_scales, const void *up_biases,
+                           const uint32_t *down_wq, const void *down_scales,
+                           const void *down_biases, int64_t n_experts, int64_t I, int64_t N,
+                           int group_size, int bits, const char *mode, qmm_activation act,
+                           void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * qmm_device_status -- synchronise `stream`, then read (and, if `reset` is
  * non-zero, clear) the library's device-side error word, set by kernels whose
  * bounded waits time out (QMM_ERR_TIMEOUT) or that meet an out-of-range index

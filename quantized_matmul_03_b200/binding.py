@@ -8,6 +8,7 @@ device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 from typing import Optional
@@ -61,6 +62,10 @@ def lib() -> ctypes.CDLL:
                                i32, i32, cp, i32, vp, vp, sz, vp],
             "qmm_gather_qmm_static": [vp, i64, i64, i64, vp, vp, vp, i32, i64, i64, vp, vp, i64,
                                       i32, i32, i32, cp, i32, vp, vp],
+            "qmm_moe_route": [vp, i32, i64, i64, vp, i32, i64, i64, i32, i64, i32, ctypes.c_double,
+                              vp, vp, vp],
+            "qmm_moe_experts": [vp, i64, i64, i32, vp, vp, i64, *[vp] * 9, i64, i64, i64, i32, i32,
+                                cp, i32, vp, vp, sz, vp],
             "qmm_device_status": [vp, i32],
             "qmm_set_path": [i32],
             "qmm_set_wait_limit_ns": [ctypes.c_uint64],
@@ -72,6 +77,8 @@ def lib() -> ctypes.CDLL:
             f.restype = ctypes.c_int
         L.qmm_qqmm_workspace_size.argtypes = [i64, i64, i32, i32, i32]
         L.qmm_qqmm_workspace_size.restype = sz
+        L.qmm_moe_experts_workspace_size.argtypes = [i64] * 6 + [i32]
+        L.qmm_moe_experts_workspace_size.restype = sz
         L.qmm_gather_qmm_workspace_size.argtypes = [i64, i64, i64, i64, i32]
         L.qmm_gather_qmm_workspace_size.restype = sz
         L.qmm_quantized_matmul_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
@@ -102,6 +109,14 @@ def _p(t: Optional[torch.Tensor]):
 
 def _stream(device: torch.device):
     return torch.cuda.current_stream(device).cuda_stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Context in which ``device`` is current (kernels launch there)."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _mode(mode: Optional[str]):
@@ -442,6 +457,103 @@ def qmm_gather_qmm_static(x, wq, scales, biases, lhs_indices=None, rhs_indices=N
                                        _p(rhs_indices), batch, int(bool(transpose)), group_size,
                                        bits, _mode(mode), int(bool(sorted_indices)), _p(out),
                                        _stream(x.device)))
+    return out
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+def qmm_moe_route(logits, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                  n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+                  renormalize: bool = True, scale: float = 1.0, out=None):
+    """Each token's experts: logits [..., E] -> (indices int32 [..., top_k],
+    weights float32 [..., top_k]), the best expert first (see include/qmm.h).
+
+    ``bias``: float32 [E], added to the scores to choose, not to weigh.
+    ``out``: optional ``(indices, weights)`` tensors to write into."""
+    _cuda(logits, bias)
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    E = logits.shape[-1]
+    T = logits.numel() // E if E else 0
+    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E or bias.device != logits.device):
+        raise ValueError(f"bias must hold {E} float32 values on the logits' device")
+    shape = tuple(logits.shape[:-1]) + (top_k,)
+    if out is None:
+        indices = torch.empty(shape, dtype=torch.int32, device=logits.device)
+        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        indices, weights = out
+        _cuda(indices, weights)
+        if (indices.dtype != torch.int32 or weights.dtype != torch.float32 or
+                indices.numel() != T * top_k or weights.numel() != T * top_k or
+                indices.device != logits.device or weights.device != logits.device):
+            raise ValueError(f"out must be int32 and float32 tensors of {T} x {top_k} on the logits' device")
+    with _on(logits.device):
+        _check(lib().qmm_moe_route(_p(logits), _dtype(logits), T, E, _p(bias), SCORES[score], n_groups,
+                                   topk_groups, group_top, top_k, int(bool(renormalize)), float(scale),
+                                   _p(indices), _p(weights), _stream(logits.device)))
+    return indices, weights
+
+
+def qmm_moe_experts_workspace_size(T: int, K: int, top_k: int, n_experts: int, I: int, N: int,
+                                   dtype=torch.bfloat16) -> int:
+    return int(lib().qmm_moe_experts_workspace_size(T, K, top_k, n_experts, I, N, DTYPES[dtype]))
+
+
+def qmm_moe_experts(x, indices, weights, gate, up, down, group_size: int = 64, bits: int = 4,
+                    mode: str = "affine", activation: str = "silu",
+                    workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """The experts' gated feed-forward layer on 4-bit stacked weights:
+    ``sum_j weights[t, j] * (act(x[t] @ Wg[e].T) * (x[t] @ Wu[e].T)) @ Wd[e].T``
+    with ``e = indices[t, j]`` (-1 leaves the slot out); x is [..., K],
+    indices and weights [..., top_k].
+
+    ``gate``, ``up``, ``down``: ``(wq, scales, biases)`` as qmm_quantize returns
+    them for weights [n_experts, I, K], [n_experts, I, K], [n_experts, N, I].
+    ``workspace``: a uint8 tensor of qmm_moe_experts_workspace_size(...) bytes to
+    use (one per call in flight), or None to allocate one."""
+    tensors = [x, indices, weights, *gate, *up, *down, workspace, out]
+    _cuda(*tensors)
+    if any(t is not None and t.device != x.device for t in tensors):
+        raise ValueError("every tensor must be on x's device")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    if indices.dtype != torch.int32 or weights.dtype != torch.float32:
+        raise ValueError("indices must be int32 and weights float32")
+    K = x.shape[-1]
+    T = x.numel() // K if K else 0
+    top_k = indices.shape[-1]
+    if indices.shape != weights.shape or indices.numel() != T * top_k:
+        raise ValueError(f"indices and weights must be [{T}, top_k]")
+    for w in (gate, up, down):
+        if w[0].dim() != 3 or w[0].dtype != torch.int32 or w[1].dim() != 3:
+            raise ValueError("expert weights are stacked [n_experts, rows, words] int32 with scales [n_experts, rows, groups]")
+    n_experts, I = gate[0].shape[0], gate[0].shape[1]
+    N = down[0].shape[1]
+    if mode not in MX_MODES and mode != "affine":
+        raise ValueError(f"unknown mode {mode}")
+    sdt = torch.uint8 if mode in MX_MODES else x.dtype
+    for name, w, rows, cols in (("gate", gate, I, K), ("up", up, I, K), ("down", down, N, I)):
+        if tuple(w[0].shape) != (n_experts, rows, cols * bits // 32):
+            raise ValueError(f"{name}: packed weight must be {(n_experts, rows, cols * bits // 32)}")
+        for s in w[1:]:
+            if s is not None and (tuple(s.shape) != (n_experts, rows, cols // group_size) or s.dtype != sdt):
+                raise ValueError(f"{name}: scales and biases must be {(n_experts, rows, cols // group_size)} {sdt}")
+    if out is None:
+        out = torch.empty(tuple(x.shape[:-1]) + (N,), dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or out.numel() != T * N:
+        raise ValueError(f"out must hold {T} x {N} values of {x.dtype}")
+    with _on(x.device):
+        if workspace is None:
+            workspace = torch.empty(qmm_moe_experts_workspace_size(T, K, top_k, n_experts, I, N, x.dtype),
+                                    dtype=torch.uint8, device=x.device)
+        _check(lib().qmm_moe_experts(_p(x), T, K, _dtype(x), _p(indices), _p(weights), top_k,
+                                     *map(_p, gate), *map(_p, up), *map(_p, down), n_experts, I, N,
+                                     group_size, bits, _mode(mode), ACTIVATIONS[activation], _p(out),
+                                     _p(workspace), workspace.numel() * workspace.element_size(),
+                                     _stream(x.device)))
     return out
 
 

@@ -12,6 +12,7 @@
 #include <cstring>
 #include <string>
 
+#include "moe.cuh"
 #include "qmm_internal.cuh"
 
 namespace qmm {
@@ -645,6 +646,126 @@ qmm_status qmm_gather_qmm_static(const void *x, int64_t x_batch, int64_t M, int6
                               sorted_indices, y, scratch, QMM_GATHER_STATIC_SCRATCH_BYTES, stream);
     } catch (...) {
         return fail(QMM_ERR_CUDA, "unexpected exception in qmm_gather_qmm_static");
+    }
+}
+
+qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t T, int64_t E, const float *bias,
+                         qmm_score score, int64_t n_groups, int64_t topk_groups, int group_top,
+                         int64_t top_k, int renormalize, double scale, int32_t *indices,
+                         float *weights, void *stream) {
+    try {
+        if (dtype != QMM_F32 && dtype != QMM_BF16 && dtype != QMM_F16)
+            return fail(QMM_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+        if (score != QMM_SCORE_SOFTMAX && score != QMM_SCORE_SIGMOID)
+            return fail(QMM_ERR_INVALID_ARG, "unknown score %d", (int)score);
+        if (T < 0 || E < 1 || E > kMoeMaxExperts)
+            return fail(QMM_ERR_INVALID_ARG, "need T >= 0 and 1 <= E <= %d", kMoeMaxExperts);
+        if (n_groups < 1 || n_groups > 32 || E % n_groups != 0)
+            return fail(QMM_ERR_INVALID_ARG, "n_groups must divide E and be at most 32 (got %lld of %lld)",
+                        (long long)n_groups, (long long)E);
+        if (topk_groups < 1 || topk_groups > n_groups)
+            return fail(QMM_ERR_INVALID_ARG, "topk_groups must be 1..n_groups (got %lld)", (long long)topk_groups);
+        if (group_top != 1 && group_top != 2)
+            return fail(QMM_ERR_INVALID_ARG, "group_top must be 1 or 2 (got %d)", group_top);
+        if (top_k < 1 || top_k > kMoeMaxTopK || top_k > topk_groups * (E / n_groups))
+            return fail(QMM_ERR_INVALID_ARG, "top_k must be 1..min(%d, %lld) (got %lld)", kMoeMaxTopK,
+                        (long long)(topk_groups * (E / n_groups)), (long long)top_k);
+        if (!std::isfinite(scale)) return fail(QMM_ERR_INVALID_ARG, "scale must be finite");
+        if (T == 0) return QMM_OK;
+        if (T > (int64_t)INT32_MAX) return fail(QMM_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens");
+        const uintptr_t lmask = dtype == QMM_F32 ? 3 : 1;
+        if (logits == nullptr || (reinterpret_cast<uintptr_t>(logits) & lmask))
+            return fail(QMM_ERR_INVALID_ARG, "logits is NULL or not aligned to its element size");
+        if (reinterpret_cast<uintptr_t>(bias) & 3)
+            return fail(QMM_ERR_INVALID_ARG, "bias is not 4-byte aligned");
+        if (indices == nullptr || weights == nullptr ||
+            ((reinterpret_cast<uintptr_t>(indices) | reinterpret_cast<uintptr_t>(weights)) & 3))
+            return fail(QMM_ERR_INVALID_ARG, "indices or weights is NULL or not 4-byte aligned");
+        RouteArgs a{logits, T, (int)E, (int)top_k, bias, (int)score, (int)n_groups, (int)topk_groups,
+                    group_top, renormalize != 0, scale, indices, weights};
+        return finish_launch(launch_moe_route(dtype, a, (cudaStream_t)stream), "moe_route launch");
+    } catch (...) {
+        return fail(QMM_ERR_CUDA, "unexpected exception in qmm_moe_route");
+    }
+}
+
+size_t qmm_moe_experts_workspace_size(int64_t T, int64_t K, int64_t top_k, int64_t n_experts, int64_t I,
+                                      int64_t N, qmm_dtype dtype) {
+    if (T <= 0 || K <= 0 || I <= 0 || N <= 0 || top_k < 1 || top_k > kMoeMaxTopK) return 0;
+    if (n_experts < 1 || n_experts > kMoeMaxExperts || (dtype != QMM_BF16 && dtype != QMM_F16)) return 0;
+    if (T > (1 << 30) / top_k || K > (1 << 24) || I > (1 << 24) || N > (1 << 24)) return 0;
+    ExpertsArgs a{};
+    a.T = T;
+    a.K = K;
+    a.top_k = (int)top_k;
+    a.n_experts = n_experts;
+    a.I = I;
+    a.N = N;
+    return moe_experts_workspace(a);
+}
+
+qmm_status qmm_moe_experts(const void *x, int64_t T, int64_t K, qmm_dtype dtype, const int32_t *indices,
+                           const float *weights, int64_t top_k, const uint32_t *gate_wq,
+                           const void *gate_scales, const void *gate_biases, const uint32_t *up_wq,
+                           const void *up_scales, const void *up_biases, const uint32_t *down_wq,
+                           const void *down_scales, const void *down_biases, int64_t n_experts,
+                           int64_t I, int64_t N, int group_size, int bits, const char *mode,
+                           qmm_activation act, void *y, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+    try {
+        int md = QMM_MODE_AFFINE;
+        qmm_status st = check_common(dtype, group_size, bits, mode, &md);
+        if (st != QMM_OK) return st;
+        if (act != QMM_ACT_SILU && act != QMM_ACT_GELU_TANH)
+            return fail(QMM_ERR_INVALID_ARG, "unknown activation %d", (int)act);
+        if (T < 0 || N < 0 || K <= 0 || I <= 0)
+            return fail(QMM_ERR_INVALID_ARG, "sizes must satisfy T >= 0, N >= 0, K > 0, I > 0");
+        if (n_experts < 1 || n_experts > kMoeMaxExperts)
+            return fail(QMM_ERR_INVALID_ARG, "n_experts must be 1..%d", kMoeMaxExperts);
+        if (top_k < 1 || top_k > kMoeMaxTopK)
+            return fail(QMM_ERR_INVALID_ARG, "top_k must be 1..%d", kMoeMaxTopK);
+        if (K % group_size != 0 || I % group_size != 0)
+            return fail(QMM_ERR_INVALID_ARG, "K and I must be multiples of group_size %d", group_size);
+        if (bits != 4 || dtype == QMM_F32 || K % 64 != 0 || I % 64 != 0)
+            return fail(QMM_ERR_UNSUPPORTED,
+                        "the experts' product takes 4-bit weights, bf16/f16 activations, and K and I in "
+                        "multiples of 64");
+        if (T > (1 << 30) / top_k || K > (1 << 24) || I > (1 << 24) || n_experts * I > (1 << 30) ||
+            n_experts * N > (1 << 30))
+            return fail(QMM_ERR_UNSUPPORTED, "sizes beyond 2^30 slots or stacked rows");
+        if (T == 0 || N == 0) return QMM_OK;
+        QMM_CHECK_PTR(x, "x");
+        QMM_CHECK_PTR(y, "y");
+        QMM_CHECK_PTR(gate_wq, "gate_wq");
+        QMM_CHECK_PTR(gate_scales, "gate_scales");
+        QMM_CHECK_PTR(up_wq, "up_wq");
+        QMM_CHECK_PTR(up_scales, "up_scales");
+        QMM_CHECK_PTR(down_wq, "down_wq");
+        QMM_CHECK_PTR(down_scales, "down_scales");
+        if (md != QMM_MODE_AFFINE) {
+            if (gate_biases != nullptr || up_biases != nullptr || down_biases != nullptr)
+                return fail(QMM_ERR_INVALID_ARG, "biases must be NULL in a microscaled mode");
+        } else {
+            QMM_CHECK_PTR(gate_biases, "gate_biases");
+            QMM_CHECK_PTR(up_biases, "up_biases");
+            QMM_CHECK_PTR(down_biases, "down_biases");
+        }
+        if (indices == nullptr || weights == nullptr ||
+            ((reinterpret_cast<uintptr_t>(indices) | reinterpret_cast<uintptr_t>(weights)) & 3))
+            return fail(QMM_ERR_INVALID_ARG, "indices or weights is NULL or not 4-byte aligned");
+        ExpertsArgs a{x, T, K, indices, weights, (int)top_k, {gate_wq, gate_scales, gate_biases},
+                      {up_wq, up_scales, up_biases}, {down_wq, down_scales, down_biases},
+                      n_experts, I, N, group_size, md, (int)act, y, workspace};
+        const size_t need = moe_experts_workspace(a);
+        if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+            return fail(QMM_ERR_WORKSPACE, "workspace must be a 256-byte aligned device buffer");
+        if (workspace_bytes < need)
+            return fail(QMM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+        if (g_path == QMM_PATH_DECODE_TC)
+            return fail(QMM_ERR_UNSUPPORTED, "the decode tensor-core path does not take experts");
+        return finish_launch(launch_moe_gemv(dtype, a, (cudaStream_t)stream), "moe_experts launch");
+    } catch (...) {
+        return fail(QMM_ERR_CUDA, "unexpected exception in qmm_moe_experts");
     }
 }
 

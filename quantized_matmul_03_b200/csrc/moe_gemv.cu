@@ -1,0 +1,441 @@
+// moe_gemv.cu -- the experts' products for few rows (single tokens, small
+// decode batches):
+//   h[p] = act(x[t] Wg[e]^T) * (x[t] Wu[e]^T)   for each slot p = (t, j), e = indices[p]
+//   y[t] = sum_j weights[t, j] (h[t, j] Wd[e]^T)
+// in two kernels, both of one shape: CTA c owns a range of output rows of
+// every expert; a unit is (slot, stretch of 1024 contraction elements); a warp
+// takes a unit, holds its 32 activations per lane in registers, and streams the
+// unit's piece of each of the CTA's rows (512 contiguous bytes of codes) past
+// them.  The pieces of a row meet in shared memory and are added in a fixed
+// order, so that results repeat bit for bit; the second kernel also adds a
+// token's slots there, weighted, and rounds once.
+//
+// Arithmetic.  32 activations are held as 16-bit integers over a common power
+// of two (error at most 2^-15 of the largest of the 32), codes are small
+// integers, and DP2A sums their products exactly: 4-bit affine codes as they
+// are, E2M1 codes doubled (an integer in [-12, 12]) and offset by 128, which
+// -128 sum(x_int) takes out again.  The integer sum is scaled by the group's
+// scale in fp32.  Between the kernels h stays in fp32.
+//
+// Bound: memory.  Every code is read once per slot, 16 bytes per lane and load,
+// two batches of eight loads in flight per warp.
+#include "moe.cuh"
+#include "mx.cuh"
+#include "ptx_sm100.cuh"
+
+namespace qmm {
+namespace {
+
+constexpr int kSeg = 1024;     // contraction elements of a unit: 32 lanes x 32 codes
+constexpr int kMaxWarps = 16;
+constexpr int kLoads = 8;      // 16-byte code loads per lane and batch
+constexpr int kPartBytes = 96 * 1024;  // partial sums of a CTA at most
+
+struct GemvParams {
+    const void *x;         // first kernel: [T, K]; second: h [P, I] fp32
+    ExpertWeight w[2];     // gate and up, or down twice
+    const int32_t *indices;
+    const float *weights;
+    void *out;             // h [P, I] fp32, or y [T, N]
+    int P, top_k, E;
+    int64_t C, R;          // contraction length, output rows of an expert
+    int rows_cta, S, units, unit_warps, row_splits;
+    int gs_log, act;
+    int *err;
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ int dp2a_lo(int xa, uint32_t b, int c) {
+    int d;
+    asm("dp2a.lo.s32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(xa), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ int dp2a_hi(int xa, uint32_t b, int c) {
+    int d;
+    asm("dp2a.hi.s32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(xa), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Eight E2M1 codes as unsigned bytes 128 + 2 e, four per word: a byte
+// permutation of the table of doubled magnitudes by the raw nibbles gives the
+// magnitude of every non-negative code and 0 for a negative one (selector bit
+// 3 asks for the sign of a table byte), by the nibbles with their sign bits
+// flipped the converse; 128 + pos - neg cannot borrow between bytes.
+__device__ __forceinline__ void e2m1_bytes(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    constexpr uint32_t A = 0x03020100u, B = 0x0C080604u;
+    const uint32_t n = w ^ 0x88888888u;
+    lo = prmt(A, B, w) + 0x80808080u - prmt(A, B, n);
+    hi = prmt(A, B, w >> 16) + 0x80808080u - prmt(A, B, n >> 16);
+}
+
+// A lane's 32 activations: pairs of 16-bit integers in the order in which DP2A
+// meets the codes, their scale 2^-sh, and the sums that the bias (affine) or
+// the offset of the codes (E2M1; two groups for nvfp4) needs.
+struct Slice {
+    int x[16];
+    float unit;      // 2^-sh; NaN if any activation is infinite or NaN
+    float xsum;      // affine: sum of the activations
+    int off[2];      // E2M1: -128 * sum of the integers of each half
+};
+
+// Element of half h (0, 1) of pair k within a word of eight codes.  Affine
+// words split into two planes of four bytes (even and odd codes).
+template <int MODE>
+__host__ __device__ constexpr int pair_elem(int k, int h) {
+    return MODE == QMM_MODE_AFFINE ? (k & 1) * 4 + h * 2 + (k >> 1) : 2 * k + h;
+}
+
+template <typename X>
+__device__ __forceinline__ void load_slice(const X *x, bool ok, float (&f)[32]) {
+    if constexpr (sizeof(X) == 4) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float4 r = ok ? *reinterpret_cast<const float4 *>(x + 4 * c) : make_float4(0, 0, 0, 0);
+            f[4 * c] = r.x;
+            f[4 * c + 1] = r.y;
+            f[4 * c + 2] = r.z;
+            f[4 * c + 3] = r.w;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 r = ok ? *reinterpret_cast<const uint4 *>(x + 8 * c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const X lo = *reinterpret_cast<const X *>(&w[q]);
+                const X hi = *(reinterpret_cast<const X *>(&w[q]) + 1);
+                f[8 * c + 2 * q] = Dt<X>::to_f(lo);
+                f[8 * c + 2 * q + 1] = Dt<X>::to_f(hi);
+            }
+        }
+    }
+}
+
+template <int MODE>
+__device__ __forceinline__ void make_slice(const float (&f)[32], Slice &s) {
+    uint32_t mb = 0;  // largest |x| by bit pattern (infinities and NaN largest)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) mb = max(mb, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    // largest < 2^ex; x 2^sh < 2^14 with sh = 14 - ex, kept where 2^sh and
+    // 2^-sh are normal floats.
+    const int ex = (int)(mb >> 23) - 126;
+    const int sh = min(126, max(-126, 14 - ex));
+    const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
+    s.unit = mb >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(127 - sh) << 23);
+    // rint(x 2^sh) by adding 1.5 * 2^23: the sum's low 16 bits are the
+    // integer's two's complement, and sums of the words give sums of the
+    // integers once the offsets are taken out.
+    uint32_t sum[2] = {0u, 0u};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a = __float_as_uint(__fmaf_rn(f[8 * w + pair_elem<MODE>(k, 0)], up, 12582912.0f));
+            const uint32_t b = __float_as_uint(__fmaf_rn(f[8 * w + pair_elem<MODE>(k, 1)], up, 12582912.0f));
+            s.x[4 * w + k] = (int)__byte_perm(a, b, 0x5410);
+            sum[w >> 1] += a + b;
+        }
+    }
+    const int s0 = (int)(sum[0] - 16u * 0x4B400000u), s1 = (int)(sum[1] - 16u * 0x4B400000u);
+    s.xsum = s.unit * (float)(s0 + s1);
+    if constexpr (MODE == QMM_MODE_NVFP4) {
+        s.off[0] = -128 * s0;
+        s.off[1] = -128 * s1;
+    } else {
+        s.off[0] = -128 * (s0 + s1);
+        s.off[1] = 0;
+    }
+}
+
+// The slice's product with 32 codes of one weight row; sb: the raw scale bits
+// (mxfp4: one byte; nvfp4: two bytes; affine: scale | bias << 16).
+template <typename T, int MODE>
+__device__ __forceinline__ float dot_slice(const Slice &s, const uint4 &w, uint32_t sb) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (MODE == QMM_MODE_AFFINE) {
+        int a0 = 0, a1 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t p0 = ws[i] & 0x0F0F0F0Fu, p1 = (ws[i] >> 4) & 0x0F0F0F0Fu;
+            a0 = dp2a_lo(s.x[4 * i], p0, a0);
+            a1 = dp2a_hi(s.x[4 * i + 1], p0, a1);
+            a0 = dp2a_lo(s.x[4 * i + 2], p1, a0);
+            a1 = dp2a_hi(s.x[4 * i + 3], p1, a1);
+        }
+        const uint16_t sh = (uint16_t)sb, bh = (uint16_t)(sb >> 16);
+        const float sc = Dt<T>::to_f(*reinterpret_cast<const T *>(&sh));
+        const float bi = Dt<T>::to_f(*reinterpret_cast<const T *>(&bh));
+        // (scale * 2^-sh) first: the integer sum times 2^-sh alone could leave
+        // the fp32 range for activations near the top of bf16's.
+        return __fmaf_rn(sc * s.unit, (float)(a0 + a1), bi * s.xsum);
+    } else {
+        constexpr bool NV = MODE == QMM_MODE_NVFP4;
+        int a0 = s.off[0], a1 = 0, b0 = s.off[1], b1 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t lo, hi;
+            e2m1_bytes(ws[i], lo, hi);
+            int &c0 = (NV && i >= 2) ? b0 : a0;
+            int &c1 = (NV && i >= 2) ? b1 : a1;
+            c0 = dp2a_lo(s.x[4 * i], lo, c0);
+            c1 = dp2a_hi(s.x[4 * i + 1], lo, c1);
+            c0 = dp2a_lo(s.x[4 * i + 2], hi, c0);
+            c1 = dp2a_hi(s.x[4 * i + 3], hi, c1);
+        }
+        const float x0 = 0.5f * mxf::scale_value<MODE>(sb & 0xFFu);
+        float c = (x0 * s.unit) * (float)(a0 + a1);
+        if constexpr (NV) {
+            const float x1 = 0.5f * mxf::scale_value<MODE>((sb >> 8) & 0xFFu);
+            c = __fmaf_rn(x1 * s.unit, (float)(b0 + b1), c);
+        }
+        return c;
+    }
+}
+
+// Sum of each v[0..8) over the 32 lanes; lane l returns the total of v[l % 8].
+__device__ __forceinline__ float reduce8(float (&v)[8], int lane) {
+#pragma unroll
+    for (int s = 4; s >= 1; s >>= 1) {
+        const bool upper = (lane & s) != 0;
+#pragma unroll
+        for (int j = 0; j < s; ++j) {
+            const float send = upper ? v[j] : v[j + s];
+            const float keep = upper ? v[j + s] : v[j];
+            v[j] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+    }
+    float r = v[0];
+    r += __shfl_xor_sync(0xffffffffu, r, 8);
+    r += __shfl_xor_sync(0xffffffffu, r, 16);
+    return r;
+}
+
+// X: type of the activations (T, or float for h).  GLU: the first kernel.
+template <typename T, typename X, int MODE, bool GLU>
+__global__ void __launch_bounds__(32 * kMaxWarps, 1) moe_gemv_kernel(const GemvParams p) {
+    constexpr int NM = GLU ? 2 : 1;       // matrices a row is taken from
+    constexpr int RB = kLoads / NM;       // rows per batch
+    extern __shared__ float part[];       // [unit][row][NM]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r0 = (int64_t)blockIdx.x * p.rows_cta;
+    const int nr = (int)min((int64_t)p.rows_cta, p.R - r0);
+    const int uw = warp % p.unit_warps, rw = warp / p.unit_warps;
+    const int per = (nr + p.row_splits - 1) / p.row_splits;
+    const int ra = min(nr, rw * per), rb = min(nr, ra + per);
+    const int64_t row_bytes = p.C / 2;
+    const int64_t gpr = p.C >> p.gs_log;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+
+    for (int u = uw; u < p.units; u += p.unit_warps) {
+        const int slot = u / p.S, seg = u - slot * p.S;
+        const int e = moe_expert(p.indices, slot, p.E, blockIdx.x == 0 && lane == 0 ? p.err : nullptr);
+        if (e < 0) continue;
+        const int64_t k0 = (int64_t)seg * kSeg + lane * 32;
+        const bool ok = k0 < p.C;
+        const uint8_t *wbase[NM];
+        const uint8_t *sbase[NM], *bbase[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const int64_t row = (int64_t)e * p.R + r0;
+            wbase[m] = reinterpret_cast<const uint8_t *>(p.w[m].wq) + row * row_bytes + k0 / 2;
+            const int64_t g = row * gpr + (k0 >> p.gs_log);
+            constexpr int SB = MODE == QMM_MODE_AFFINE ? 2 : 1;
+            sbase[m] = static_cast<const uint8_t *>(p.w[m].scales) + SB * g;
+            bbase[m] = MODE == QMM_MODE_AFFINE ? static_cast<const uint8_t *>(p.w[m].biases) + SB * g : nullptr;
+        }
+        uint4 wv[2][kLoads];
+        uint32_t sv[2][kLoads];
+        auto fetch = [&](int r, uint4 (&w)[kLoads], uint32_t (&s)[kLoads]) {
+#pragma unroll
+            for (int j = 0; j < RB; ++j) {
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    const int i = j * NM + m;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    s[i] = 0;
+                    if (ok && r + j < rb) {
+                        w[i] = ld_stream(wbase[m] + (int64_t)(r + j) * row_bytes);
+                        if constexpr (MODE == QMM_MODE_AFFINE) {
+                            const int64_t o = (int64_t)(r + j) * gpr * 2;
+                            s[i] = (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(sbase[m] + o)) |
+                                   ((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(bbase[m] + o)) << 16);
+                        } else if constexpr (MODE == QMM_MODE_NVFP4) {
+                            s[i] = __ldg(reinterpret_cast<const uint16_t *>(sbase[m] + (int64_t)(r + j) * gpr));
+                        } else {
+                            s[i] = __ldg(sbase[m] + (int64_t)(r + j) * gpr);
+                        }
+                    }
+                }
+            }
+        };
+        if (ra < rb) fetch(ra, wv[0], sv[0]);
+        Slice sl;
+        {
+            float f[32];
+            const int64_t xr = GLU ? slot / p.top_k : slot;
+            load_slice<X>(static_cast<const X *>(p.x) + xr * p.C + k0, ok, f);
+            make_slice<MODE>(f, sl);
+        }
+        auto use = [&](int r, const uint4 (&w)[kLoads], const uint32_t (&s)[kLoads]) {
+            float v[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) v[i] = ok ? dot_slice<T, MODE>(sl, w[i], s[i]) : 0.f;
+            const float t = reduce8(v, lane);
+            if (lane < kLoads && r + lane / NM < rb)
+                part[((int64_t)u * p.rows_cta + r) * NM + lane] = t;
+        };
+        for (int r = ra; r < rb; r += 2 * RB) {
+            if (r + RB < rb) fetch(r + RB, wv[1], sv[1]);
+            use(r, wv[0], sv[0]);
+            if (r + RB < rb) {
+                if (r + 2 * RB < rb) fetch(r + 2 * RB, wv[0], sv[0]);
+                use(r + RB, wv[1], sv[1]);
+            }
+        }
+    }
+    __syncthreads();
+    if constexpr (GLU) {
+        float *h = static_cast<float *>(p.out);
+        for (int i = threadIdx.x; i < p.P * nr; i += blockDim.x) {
+            const int slot = i / nr, r = i - slot * nr;
+            if (moe_expert(p.indices, slot, p.E, nullptr) < 0) continue;
+            float g = 0.f, up = 0.f;
+            for (int s = 0; s < p.S; ++s) {
+                const float *q = part + ((int64_t)(slot * p.S + s) * p.rows_cta + r) * 2;
+                g += q[0];
+                up += q[1];
+            }
+            h[(int64_t)slot * p.R + r0 + r] = moe_gate(g, p.act) * up;
+        }
+    } else {
+        const int T_ = p.P / p.top_k;
+        for (int i = threadIdx.x; i < T_ * nr; i += blockDim.x) {
+            const int t = i / nr, r = i - t * nr;
+            float acc = 0.f;
+            for (int j = 0; j < p.top_k; ++j) {
+                const int slot = t * p.top_k + j;
+                if (moe_expert(p.indices, slot, p.E, nullptr) < 0) continue;
+                float d = 0.f;
+                for (int s = 0; s < p.S; ++s) d += part[(int64_t)(slot * p.S + s) * p.rows_cta + r];
+                acc = __fmaf_rn(__ldg(p.weights + slot), d, acc);
+            }
+            static_cast<T *>(p.out)[(int64_t)t * p.R + r0 + r] = Dt<T>::from_f(acc);
+        }
+    }
+}
+
+template <typename T, typename X, int MODE, bool GLU>
+cudaError_t launch_half(GemvParams p, cudaStream_t s) {
+    constexpr int NM = GLU ? 2 : 1;
+    p.S = (int)((p.C + kSeg - 1) / kSeg);
+    p.units = p.P * p.S;
+    p.unit_warps = std::min(p.units, kMaxWarps);
+    p.row_splits = kMaxWarps / p.unit_warps;
+    int64_t rows = (p.R + num_sms() - 1) / num_sms();
+    rows = std::min<int64_t>(rows, std::max<int64_t>(1, kPartBytes / ((int64_t)p.units * NM * 4)));
+    p.rows_cta = (int)rows;
+    const size_t smem = (size_t)p.units * (size_t)rows * NM * 4;
+    if (smem > 200 * 1024) return cudaErrorInvalidConfiguration;
+    auto kern = moe_gemv_kernel<T, X, MODE, GLU>;
+    struct Tag;
+    cudaError_t e = configure_once<Tag>(smem, [&]() {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.R + rows - 1) / rows), 1, 1);
+    cfg.blockDim = dim3(32 * p.unit_warps * p.row_splits, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <typename T, int MODE>
+cudaError_t run(const ExpertsArgs &a, cudaStream_t s) {
+    GemvParams p{};
+    p.indices = a.indices;
+    p.weights = a.weights;
+    p.P = (int)(a.T * a.top_k);
+    p.top_k = a.top_k;
+    p.E = (int)a.n_experts;
+    p.gs_log = a.group_size == 16 ? 4 : (a.group_size == 32 ? 5 : (a.group_size == 64 ? 6 : 7));
+    p.act = a.act;
+    p.err = device_error_word();
+    p.x = a.x;
+    p.w[0] = a.gate;
+    p.w[1] = a.up;
+    p.out = a.ws;
+    p.C = a.K;
+    p.R = a.I;
+    cudaError_t e = launch_half<T, T, MODE, true>(p, s);
+    if (e != cudaSuccess) return e;
+    p.x = a.ws;
+    p.w[0] = p.w[1] = a.down;
+    p.out = a.y;
+    p.C = a.I;
+    p.R = a.N;
+    return launch_half<T, float, MODE, false>(p, s);
+}
+
+template <typename T>
+cudaError_t run_mode(const ExpertsArgs &a, cudaStream_t s) {
+    switch (a.mode) {
+    case QMM_MODE_AFFINE: return run<T, QMM_MODE_AFFINE>(a, s);
+    case QMM_MODE_MXFP4: return run<T, QMM_MODE_MXFP4>(a, s);
+    default: return run<T, QMM_MODE_NVFP4>(a, s);
+    }
+}
+
+// Tokens of one pass: about 64 slots, fewer for contractions so long that the
+// partial sums of one row would pass a CTA's share of shared memory.
+int64_t block_tokens(const ExpertsArgs &a) {
+    const int64_t S = (std::max(a.K, a.I) + kSeg - 1) / kSeg;
+    const int64_t slots = std::max<int64_t>(a.top_k, std::min<int64_t>(64, kPartBytes / (8 * S)));
+    return std::max<int64_t>(1, slots / a.top_k);
+}
+
+}  // namespace
+
+size_t moe_gemv_workspace(const ExpertsArgs &a) {
+    return (size_t)(std::min<int64_t>(a.T, block_tokens(a)) * a.top_k) * (size_t)a.I * 4;
+}
+
+size_t moe_experts_workspace(const ExpertsArgs &a) { return moe_gemv_workspace(a); }
+
+cudaError_t launch_moe_gemv(qmm_dtype dt, const ExpertsArgs &a, cudaStream_t s) {
+    const int64_t step = block_tokens(a);
+    for (int64_t t = 0; t < a.T; t += step) {
+        ExpertsArgs b = a;
+        b.T = std::min(step, a.T - t);
+        b.x = static_cast<const char *>(a.x) + t * a.K * 2;
+        b.y = static_cast<char *>(a.y) + t * a.N * 2;
+        b.indices = a.indices + t * a.top_k;
+        b.weights = a.weights + t * a.top_k;
+        const cudaError_t e = dt == QMM_BF16 ? run_mode<__nv_bfloat16>(b, s) : run_mode<__half>(b, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace qmm

@@ -126,6 +126,9 @@ bool gather_tc_supported(qmm_dtype dtype, int64_t x_batch, int64_t M, int64_t K,
     return gemm_grouped_supported(dtype, probe) && gather_prep_fits(n_experts);
 }
 
+// Slots up to which qmm_moe_experts takes the few-row kernels.
+constexpr int64_t kMoeGemvSlots = 16;
+
 qmm_status finish_launch(cudaError_t e, const char *what) {
     if (e != cudaSuccess) return cuda_fail(e, what);
     return QMM_OK;
@@ -144,6 +147,11 @@ cudaError_t launch_mx_matmul(qmm_dtype dt, const QmmArgs &a, cudaStream_t s) {
     if (gemv_fast_supported(dt, a)) return launch_gemv_fast(dt, a, s);
     if (gemm_supported(dt, a)) return launch_gemm(dt, a, s);
     return launch_gemv(dt, a, s);
+}
+
+// Every path fits, whichever qmm_set_path selects later.
+size_t moe_experts_workspace(const ExpertsArgs &a) {
+    return std::max(moe_gemv_workspace(a), moe_tc_workspace(a));
 }
 
 static std::atomic<uint64_t> g_launches{0};
@@ -763,7 +771,12 @@ qmm_status qmm_moe_experts(const void *x, int64_t T, int64_t K, qmm_dtype dtype,
             return fail(QMM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
         if (g_path == QMM_PATH_DECODE_TC)
             return fail(QMM_ERR_UNSUPPORTED, "the decode tensor-core path does not take experts");
-        return finish_launch(launch_moe_gemv(dtype, a, (cudaStream_t)stream), "moe_experts launch");
+        const bool few = g_path == QMM_PATH_GEMV || (g_path == QMM_PATH_AUTO && T * top_k <= kMoeGemvSlots);
+        if (few || (g_path == QMM_PATH_AUTO && !moe_tc_supported()))
+            return finish_launch(launch_moe_gemv(dtype, a, (cudaStream_t)stream), "moe_experts launch");
+        if (!moe_tc_supported())
+            return fail(QMM_ERR_UNSUPPORTED, "the tensor-core path needs the driver's tensor maps");
+        return finish_launch(launch_moe_tc(dtype, a, (cudaStream_t)stream), "moe_experts launch");
     } catch (...) {
         return fail(QMM_ERR_CUDA, "unexpected exception in qmm_moe_experts");
     }

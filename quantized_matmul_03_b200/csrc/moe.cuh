@@ -50,6 +50,10 @@ size_t moe_experts_workspace(const ExpertsArgs &a);
 // tokens than one pass takes go through in blocks.
 size_t moe_gemv_workspace(const ExpertsArgs &a);
 cudaError_t launch_moe_gemv(qmm_dtype dt, const ExpertsArgs &a, cudaStream_t s);
+// Many rows: sort by expert and two grouped tensor-core products.
+bool moe_tc_supported();
+size_t moe_tc_workspace(const ExpertsArgs &a);
+cudaError_t launch_moe_tc(qmm_dtype dt, const ExpertsArgs &a, cudaStream_t s);
 
 // Gated activation in fp32.
 __device__ __forceinline__ float moe_gate(float g, int act) {

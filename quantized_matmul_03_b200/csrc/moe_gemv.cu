@@ -421,8 +421,6 @@ size_t moe_gemv_workspace(const ExpertsArgs &a) {
     return (size_t)(std::min<int64_t>(a.T, block_tokens(a)) * a.top_k) * (size_t)a.I * 4;
 }
 
-size_t moe_experts_workspace(const ExpertsArgs &a) { return moe_gemv_workspace(a); }
-
 cudaError_t launch_moe_gemv(qmm_dtype dt, const ExpertsArgs &a, cudaStream_t s) {
     const int64_t step = block_tokens(a);
     for (int64_t t = 0; t < a.T; t += step) {

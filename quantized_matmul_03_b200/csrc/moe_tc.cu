@@ -1,0 +1,942 @@
+// moe_tc.cu -- the experts' products for many rows, on the tensor cores:
+//   h[p] = act(x[t] Wg[e]^T) * (x[t] Wu[e]^T)   for each slot p = (t, j), e = indices[p]
+//   y[t] = sum_j weights[t, j] (h[t, j] Wd[e]^T)
+//
+// Kernels of one call:
+//   1. prep      slots ordered by expert (stable), each expert's rows cut into
+//                chunks of at most `cap` rows, and x copied into that order;
+//   2. gate/up   grouped product with the gated activation in its epilogue;
+//   3. down      grouped product, one fp32 row per slot;
+//   4. combine   a token's rows added in slot order with their weights and
+//                rounded once.
+// Both products are moe_tc_kernel.  Everything lies in the caller's workspace.
+//
+// The product.  D[n, m] (+)= W~[n, k] x[m, k]: 128 weight rows are the MMA's M,
+// up to 192 activation rows its N, k runs in blocks of 64.  The packed weight is
+// dequantized on chip into tensor memory (operand A); the activations are
+// operand B in shared memory.  The first product's 128 rows are 64 gate and 64
+// up rows, placed so that the two rows of a feature are 16 lanes apart in one
+// warp: the epilogue exchanges halves by shuffle and writes h once.
+//
+// Order of k.  One 32-bit word holds codes 0..7; masks and shifts give codes e
+// and e + 4 in the two halves of a register, so a block's elements enter the
+// MMA in the order 0 4 1 5 2 6 3 7 of every eight.  The sum does not depend on
+// it: x is copied, and h written, in the same order.
+//
+// E2M1 to 16 bits.  Sign, exponent and mantissa bits of a code land in a
+// register half as a number 2^-126 (bf16) or 2^-14 (f16) times its value,
+// subnormals included, and one packed multiply by X 2^126 (X 2^14) gives
+// X * element exactly.  Scales for which that factor leaves the type's range
+// take the element values in fp32 instead.
+//
+// Roles (one CTA per SM, 25 warps, persistent over chunk x 128-row tiles):
+//   0-15   dequantize, four groups of four warps; group g takes block g of each
+//          four, thread r of a group owns weight row r;
+//   16-19  epilogue;  20 MMA issuer, owner of tensor memory;
+//   21, 22 TMA of packed tiles (gate and up, or the down tile), 256 k at a time;
+//   23     TMA of activation tiles;
+//   24     scale (and bias) windows of 16 bytes a row, by asynchronous copies.
+// Three rings: packed tiles and windows, activation tiles, and dequantized
+// blocks in tensor memory.  TMA issues cost their thread several hundred cycles
+// each whatever their size, so a packed tile is 256 elements wide and an
+// activation tile comes in one box as high as the chunk needs (heights in
+// kHeights).
+//
+// Bound: with few rows per expert the dequantize warps' integer instructions
+// (about 3 per element), above HBM's time by half; with many rows the tensor
+// cores.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "moe.cuh"
+#include "mx.cuh"
+#include "ptx_sm100.cuh"
+#include "tcgen05.cuh"
+
+namespace qmm {
+namespace {
+
+constexpr int kGroups = 4;
+constexpr int kDqWarps = 4 * kGroups;
+constexpr int kEpiWarp = kDqWarps;        // 16..19
+constexpr int kMmaWarp = kEpiWarp + 4;    // 20
+constexpr int kWWarp = kMmaWarp + 1;      // 21, 22
+constexpr int kBWarp = kWWarp + 2;        // 23
+constexpr int kSWarp = kBWarp + 1;        // 24
+constexpr int kThreads = 32 * (kSWarp + 1);
+constexpr int kBM = 128, kBK = 64;
+constexpr int kStageK = kBK * kGroups;    // k per packed stage
+constexpr int kPBytes = kBM * kStageK / 2;  // 16 KB
+constexpr int kWinBytes = kBM * 16;       // one window of 16 bytes per row
+constexpr int kNumHeights = 6;
+constexpr int kHeights[kNumHeights] = {16, 32, 64, 96, 128, 192};
+
+struct MoeHeader {
+    int num_chunks;
+    int valid;  // slots with an expert (sorted first)
+};
+
+struct MoePlan {
+    size_t hdr, chunks, perm, x, h, parts, total;
+    int64_t max_chunks;
+};
+
+struct ActMaps {
+    CUtensorMap m[kNumHeights];
+};
+
+struct TcParams {
+    const void *scales[2], *biases[2];
+    void *out;                // h [R / 64][rows][64] T, or parts [slots][R] fp32
+    int64_t row_bytes_sb;     // bytes of one row of scales
+    int rows;                 // slots
+    int R, KB, gs_log, n_tiles;
+    int acc_stride, na_log;   // columns per accumulator; log2 of A slots
+    int SP, SB, BS, b_bytes;  // ring depths, k-blocks and bytes of an activation stage
+    int sb_vec;               // scale copies of 16, 4 or 2 bytes
+    int act;
+    const MoeHeader *hdr;
+    const int4 *chunks;       // {expert, first sorted row, rows, box (box_of)}
+    const int32_t *perm;
+    int *err;
+};
+
+// ---------------------------------------------------------------------------
+// Dequantization: one word (8 codes) -> 4 registers (e, e + 4).
+// ---------------------------------------------------------------------------
+template <typename T> struct Half2;
+template <> struct Half2<__nv_bfloat16> {
+    using V = __nv_bfloat162;
+    static constexpr uint32_t MAGIC = 0x43004300u;  // 128.0, 128.0
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const V v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    static __device__ __forceinline__ uint32_t off() { return MAGIC; }
+};
+template <> struct Half2<__half> {
+    using V = __half2;
+    static constexpr uint32_t MAGIC = 0x64006400u;  // 1024.0, 1024.0
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+        const V v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    static __device__ __forceinline__ uint32_t off() { return MAGIC; }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    using V = typename Half2<T>::V;
+    const V r = __hmul2(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    using V = typename Half2<T>::V;
+    const V r = __hsub2(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+    using V = typename Half2<T>::V;
+    const V r = __hfma2(*reinterpret_cast<const V *>(&a), *reinterpret_cast<const V *>(&b),
+                        *reinterpret_cast<const V *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Codes e and e + 4 of w as 2^-126 (bf16) or 2^-14 (f16) times their values.
+template <typename T>
+__device__ __forceinline__ void e2m1_place(uint32_t w, uint32_t (&r)[4]) {
+    constexpr uint32_t S = 0x80008000u;
+    if constexpr (std::is_same<T, __half>::value) {
+        constexpr uint32_t M = 0x0E000E00u;
+        r[0] = ((w << 12) & S) | ((w << 9) & M);
+        r[1] = ((w << 8) & S) | ((w << 5) & M);
+        r[2] = ((w << 4) & S) | ((w << 1) & M);
+        r[3] = (w & S) | ((w >> 3) & M);
+    } else {
+        constexpr uint32_t M = 0x01C001C0u;
+        r[0] = ((w << 12) & S) | ((w << 6) & M);
+        r[1] = ((w << 8) & S) | ((w << 2) & M);
+        r[2] = ((w << 4) & S) | ((w >> 2) & M);
+        r[3] = (w & S) | ((w >> 6) & M);
+    }
+}
+
+// The packed factor X 2^126 (bf16) or X 2^14 (f16) of a scale byte in range.
+template <typename T, int MODE>
+__device__ __forceinline__ bool scale_in_range(uint32_t s) {
+    if constexpr (MODE == QMM_MODE_NVFP4) return (s & 0x7Fu) < 0x48u;  // |X| < 4
+    else return s <= 128u;                                             // X <= 2
+}
+template <typename T, int MODE>
+__device__ __forceinline__ uint32_t scale_factor(uint32_t s) {
+    if constexpr (MODE == QMM_MODE_NVFP4) {
+        const float x = mxf::scale_value<MODE>(s);
+        const float f = std::is_same<T, __half>::value ? x * 16384.f : x * 8.507059173e37f;  // 2^14, 2^126
+        return Half2<T>::pack(f, f);
+    } else if constexpr (std::is_same<T, __half>::value) {
+        // 2^(s - 113): normal from s = 99, subnormal down to s = 89, then 0
+        // (where X * element is below half of f16's smallest value).
+        const uint32_t b = s >= 99u ? (s - 98u) << 10 : (s >= 89u ? 1u << (s - 89u) : 0u);
+        return b * 0x00010001u;
+    } else {
+        return (s + 126u) * 0x00800080u;  // exponent field s + 126 in both halves
+    }
+}
+
+// A block of 64 elements: w[8] codes -> v[32].  sb: the block's scale bytes
+// (affine: the scales, and bb the biases, of its two halves).
+template <typename T, int MODE>
+__device__ __forceinline__ void dequant_block(const uint32_t (&w)[8], uint32_t sb, uint32_t bb,
+                                              uint32_t (&v)[32]) {
+    if constexpr (MODE == QMM_MODE_AFFINE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t s2 = __byte_perm(sb, sb, i < 4 ? 0x1010 : 0x3232);
+            const uint32_t b2 = __byte_perm(bb, bb, i < 4 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t t = ((w[i] >> (4 * e)) & 0x000F000Fu) | Half2<T>::MAGIC;
+                v[4 * i + e] = fma2<T>(sub2<T>(t, Half2<T>::off()), s2, b2);
+            }
+        }
+    } else {
+        constexpr int NG = MODE == QMM_MODE_NVFP4 ? 4 : 2;  // groups per block
+        bool fast = true;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) fast = fast && scale_in_range<T, MODE>((sb >> (8 * g)) & 0xFFu);
+        if (fast) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const uint32_t f = scale_factor<T, MODE>((sb >> (8 * g)) & 0xFFu);
+#pragma unroll
+                for (int i = g * 8 / NG; i < (g + 1) * 8 / NG; ++i) {
+                    uint32_t r[4];
+                    e2m1_place<T>(w[i], r);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[4 * i + e] = mul2<T>(r[e], f);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float x = mxf::scale_value<MODE>((sb >> (8 * (i * NG / 8))) & 0xFFu);
+                float f[8];
+                mxf::elements<MODE>(w[i], f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * i + e] = Half2<T>::pack(x * f[e], x * f[e + 4]);
+            }
+        }
+    }
+}
+
+// Gated activation for a value that is rounded to 16 bits next.
+__device__ __forceinline__ float gate_fast(float g, int act) {
+    float z = g;
+    if (act != QMM_ACT_SILU) z = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    return __fdividef(g, 1.f + __expf(-z));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrive on bar once this thread's cp.async so far have landed (counted among
+// the barrier's arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    bool wrapped = false;
+    __device__ void next(int n) {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1;
+            wrapped = true;
+        }
+    }
+};
+
+template <typename T, int MODE, bool GLU>
+__global__ void __launch_bounds__(kThreads, 1)
+moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
+              const __grid_constant__ ActMaps map_b, const __grid_constant__ TcParams p) {
+    constexpr bool AFF = MODE == QMM_MODE_AFFINE;
+    constexpr int NW = AFF ? 2 : 1;             // windows per stage: scales (and biases)
+    constexpr int NM = GLU ? 2 : 1;             // packed boxes per stage
+    constexpr uint32_t TMEM_COLS = 512;
+    constexpr bool kF16 = std::is_same<T, __half>::value;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw);
+    const int SP = p.SP, SB = p.SB, NA = 1 << p.na_log;
+    const uint32_t b0 = base, p0 = b0 + SB * p.b_bytes, s0 = p0 + SP * kPBytes;
+    const uint32_t bars = s0 + SP * NW * kWinBytes;
+    const uint32_t full_p = bars, empty_p = full_p + 8 * SP, full_b = empty_p + 8 * SP, empty_b = full_b + 8 * SB;
+    const uint32_t full_a = empty_b + 8 * SB, empty_a = full_a + 8 * NA;
+    const uint32_t acc_full = empty_a + 8 * NA, acc_empty = acc_full + 16, done = acc_empty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + (done + 8 - base));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < SP; ++i) {
+            ptx::mbar_init(full_p + 8 * i, NM + 32);
+            ptx::mbar_init(empty_p + 8 * i, kDqWarps);
+        }
+        for (int i = 0; i < SB; ++i) {
+            ptx::mbar_init(full_b + 8 * i, 1);
+            ptx::mbar_init(empty_b + 8 * i, 1);
+        }
+        for (int i = 0; i < NA; ++i) {
+            ptx::mbar_init(full_a + 8 * i, 4);
+            ptx::mbar_init(empty_a + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(acc_full + 8 * i, 1);
+            ptx::mbar_init(acc_empty + 8 * i, 4);
+        }
+        ptx::mbar_init(done, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(ptx::smem_addr(tmem_slot), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // What the preceding kernels wrote (chunks, activations) is read from here on.
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int KB = p.KB, KS = (KB + kGroups - 1) / kGroups;
+    const int num_tiles = p.hdr->num_chunks * p.n_tiles;
+    const uint32_t a_col0 = 2u * p.acc_stride;
+
+    if (warp < kDqWarps) {
+        // ------------------------- dequantize -------------------------
+        const int g = warp >> 2, q = warp & 3;
+        const int row = GLU ? 16 * q + (lane & 15) + ((lane & 16) << 2) : 32 * q + lane;
+        const uint8_t *prow = gbase + (p0 - base) + row * (kStageK / 2);
+        const uint8_t *swin = gbase + (s0 - base) + row * 16;
+        const uint32_t dst = tmem + ((uint32_t)(32 * q) << 16) + a_col0;
+        uint32_t c = 0;
+        Ring ps;
+        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+            for (int st = 0; st < KS; ++st, ps.next(SP)) {
+                const int kb = st * kGroups + g;
+                ptx::mbar_wait(full_p + 8 * ps.slot, ps.phase, p.err);
+                if (kb < KB) {
+                    uint32_t w[8], sb = 0, bb = 0;
+                    const uint8_t *src = prow + ps.slot * kPBytes;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(src + (((2 * g + i) ^ (row & 7)) << 4));
+                        w[4 * i] = u.x;
+                        w[4 * i + 1] = u.y;
+                        w[4 * i + 2] = u.z;
+                        w[4 * i + 3] = u.w;
+                    }
+                    const uint8_t *sw = swin + ps.slot * (NW * kWinBytes);
+                    if constexpr (AFF) {
+                        // first group of each half, as halves of a word
+                        const int o0 = (((kb * kBK) >> p.gs_log) * 2) & 15;
+                        const int o1 = (((kb * kBK + 32) >> p.gs_log) * 2) & 15;
+                        sb = *reinterpret_cast<const uint16_t *>(sw + o0) |
+                             ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + o1) << 16);
+                        bb = *reinterpret_cast<const uint16_t *>(sw + kWinBytes + o0) |
+                             ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + kWinBytes + o1) << 16);
+                    } else if constexpr (MODE == QMM_MODE_NVFP4) {
+                        sb = *reinterpret_cast<const uint32_t *>(sw + ((4 * kb) & 15));
+                    } else {
+                        sb = *reinterpret_cast<const uint16_t *>(sw + ((2 * kb) & 15));
+                    }
+                    uint32_t v[32];
+                    dequant_block<T, MODE>(w, sb, bb, v);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
+                    const uint32_t cc = c + kb, slot = cc & (NA - 1);
+                    if (cc >= (uint32_t)NA) ptx::mbar_wait(empty_a + 8 * slot, ((cc >> p.na_log) & 1) ^ 1, p.err);
+                    tc_fence_after();
+                    tmem_st32(dst + 32u * slot, v);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(full_a + 8 * slot);
+                } else {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
+                }
+            }
+            c += KB;
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------- epilogue -------------------------
+        const int q = warp & 3;
+        int i = 0;
+        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++i) {
+            const int acc = i & 1, use = i >> 1;
+            const int4 ch = p.chunks[tile / p.n_tiles];
+            const int nt = tile % p.n_tiles;
+            ptx::mbar_wait(acc_full + 8 * acc, use & 1, p.err);
+            tc_fence_after();
+            const int nj = (ch.z + 31) / 32;
+            for (int j = 0; j < nj; ++j) {
+                uint32_t v[32];
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + acc * p.acc_stride + 32 * j, v);
+                tmem_ld_wait();
+                if (j == nj - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(acc_empty + 8 * acc);
+                }
+                if constexpr (GLU) {
+                    // Lanes 0-15 hold gate features 16 q + lane, lanes 16-31 the
+                    // up values of the same features: the lower lanes take
+                    // columns 0-15, the upper ones 16-31.
+                    const bool upper = lane >= 16;
+                    const int f = 16 * q + (lane & 15);
+                    const int pos = (f & ~7) | ((f & 3) << 1) | ((f >> 2) & 1);
+                    T *h = static_cast<T *>(p.out) + ((int64_t)nt * p.rows + ch.y) * kBK + pos;
+#pragma unroll
+                    for (int cc = 0; cc < 16; ++cc) {
+                        const float lo = __uint_as_float(v[cc]), hi = __uint_as_float(v[cc + 16]);
+                        const float got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, 16);
+                        const float gt = upper ? got : lo, up = upper ? hi : got;
+                        const int m = 32 * j + cc + (upper ? 16 : 0);
+                        if (m < ch.z) h[(int64_t)m * kBK] = Dt<T>::from_f(gate_fast(gt, p.act) * up);
+                    }
+                } else {
+                    const int n = nt * kBM + 32 * q + lane;
+                    const int mm = 32 * j + lane;
+                    const int my = mm < ch.z ? p.perm[ch.y + mm] : 0;
+                    float *parts = static_cast<float *>(p.out) + n;
+#pragma unroll
+                    for (int cc = 0; cc < 32; ++cc) {
+                        const int64_t slot = __shfl_sync(0xffffffffu, my, cc);
+                        if (32 * j + cc < ch.z && n < p.R) parts[slot * p.R] = __uint_as_float(v[cc]);
+                    }
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------- MMA issuer -------------------------
+        const bool leader = elect_one();
+        uint32_t c = 0;
+        int i = 0;
+        Ring bs;
+        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++i) {
+            const int acc = i & 1, use = i >> 1;
+            const int4 ch = p.chunks[tile / p.n_tiles];
+            const uint32_t idesc = make_idesc(kF16, kBM, (ch.z + 15) & ~15);
+            const uint32_t zbytes = (uint32_t)(ch.w >> 8) * 128u;  // one k-block of the activation tile
+            if (leader && i >= 2) ptx::mbar_wait(acc_empty + 8 * acc, (use + 1) & 1, p.err);
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t d = tmem + acc * p.acc_stride;
+            int kz = 0;
+            for (int kb = 0; kb < KB; ++kb) {
+                const uint32_t cc = c + kb, slot = cc & (NA - 1);
+                const bool last = kz == p.BS - 1 || kb == KB - 1;
+                if (leader) {
+                    if (kz == 0) ptx::mbar_wait<false>(full_b + 8 * bs.slot, bs.phase, p.err);
+                    ptx::mbar_wait<false>(full_a + 8 * slot, (cc >> p.na_log) & 1, p.err);
+                    tc_fence_after();
+                    const uint64_t db = sw128_desc(b0 + bs.slot * p.b_bytes + kz * zbytes);
+                    const uint32_t ta = tmem + a_col0 + 32u * slot;
+                    tc_mma_ts(d, ta, db, idesc, kb != 0);
+                    tc_mma_ts(d, ta + 8, db + 2, idesc, 1);
+                    tc_mma_ts(d, ta + 16, db + 4, idesc, 1);
+                    tc_mma_ts(d, ta + 24, db + 6, idesc, 1);
+                    tc_commit(empty_a + 8 * slot);
+                    if (last) tc_commit(empty_b + 8 * bs.slot);
+                }
+                __syncwarp();
+                ++kz;
+                if (last) {
+                    kz = 0;
+                    bs.next(SB);
+                }
+            }
+            c += KB;
+            if (leader) tc_commit(acc_full + 8 * acc);
+            __syncwarp();
+        }
+        // Every MMA has completed before tensor memory is freed.
+        if (leader) {
+            tc_commit(done);
+            ptx::mbar_drain(done, 0, p.err);
+        }
+        __syncwarp();
+    } else if (warp < kBWarp) {
+        // ------------------------- packed tiles -------------------------
+        const int m = warp - kWWarp;
+        if (lane == 0 && m < NM) {
+            const CUtensorMap *map = m == 0 ? &map_w0 : &map_w1;
+            constexpr uint32_t bytes = kPBytes / NM;
+            Ring ps;
+            int n = 0;
+            for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+                const int4 ch = p.chunks[tile / p.n_tiles];
+                const int r0 = ch.x * p.R + (tile % p.n_tiles) * (kBM / NM);
+                for (int st = 0; st < KS; ++st, ++n, ps.next(SP)) {
+                    if (ps.wrapped) ptx::mbar_wait(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
+                    ptx::mbar_arrive_expect_tx(full_p + 8 * ps.slot, bytes);
+                    tma_load_2d(p0 + ps.slot * kPBytes + m * bytes, map, st * (kStageK / 8), r0,
+                                full_p + 8 * ps.slot);
+                }
+            }
+            for (int k = max(0, n - SP); k < n; ++k) ptx::mbar_drain(full_p + 8 * (k % SP), (k / SP) & 1, p.err);
+        }
+    } else if (warp == kBWarp) {
+        // ------------------------- activation tiles -------------------------
+        if (lane == 0) {
+            // the activations were written by ordinary stores of earlier kernels
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            Ring bs;
+            int n = 0;
+            for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+                const int4 ch = p.chunks[tile / p.n_tiles];
+                const CUtensorMap *map = &map_b.m[ch.w & 255];
+                const uint32_t bytes = (uint32_t)(ch.w >> 8) * 128u * p.BS;
+                for (int kb = 0; kb < KB; kb += p.BS, ++n, bs.next(SB)) {
+                    if (bs.wrapped) ptx::mbar_wait(empty_b + 8 * bs.slot, bs.phase ^ 1, p.err);
+                    ptx::mbar_arrive_expect_tx(full_b + 8 * bs.slot, bytes);
+                    tma_load_3d(b0 + bs.slot * p.b_bytes, map, 0, ch.y, kb, full_b + 8 * bs.slot);
+                }
+            }
+            for (int k = max(0, n - SB); k < n; ++k) ptx::mbar_drain(full_b + 8 * (k % SB), (k / SB) & 1, p.err);
+        }
+    } else {
+        // ------------------------- scale windows -------------------------
+        constexpr int ES = AFF ? 2 : 1;
+        Ring ps;
+        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
+            const int4 ch = p.chunks[tile / p.n_tiles];
+            const int nt = tile % p.n_tiles;
+            const uint8_t *src[4][NW];
+            bool ok[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = lane + 32 * i;
+                const int m = GLU ? i >> 1 : 0;
+                const int n = GLU ? nt * (kBM / 2) + (r & 63) : nt * kBM + r;
+                ok[i] = n < p.R;  // rows past the last expert's end are not read
+                const int64_t off = ((int64_t)ch.x * p.R + n) * p.row_bytes_sb;
+                src[i][0] = static_cast<const uint8_t *>(p.scales[m]) + off;
+                if constexpr (AFF) src[i][1] = static_cast<const uint8_t *>(p.biases[m]) + off;
+            }
+            for (int st = 0; st < KS; ++st, ps.next(SP)) {
+                if (ps.wrapped) ptx::mbar_wait(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
+                const uint32_t win = s0 + ps.slot * (NW * kWinBytes) + lane * 16;
+                const int64_t at = (((int64_t)st * kStageK) >> p.gs_log) * ES & ~15;  // window's first byte
+                const int left = (int)min((int64_t)16, p.row_bytes_sb - at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!ok[i]) continue;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        const uint32_t d = win + w * kWinBytes + i * 512;
+                        if (p.sb_vec == 16) {
+                            cp_async16(d, src[i][w] + at);
+                        } else if (p.sb_vec == 4) {
+                            for (int o = 0; o < left; o += 4) cp_async4(d + o, src[i][w] + at + o);
+                        } else {
+                            for (int o = 0; o < left; o += 2)
+                                sts16(d + o, __ldg(reinterpret_cast<const uint16_t *>(src[i][w] + at + o)));
+                        }
+                    }
+                }
+                if (p.sb_vec == 2) ptx::mbar_arrive(full_p + 8 * ps.slot);
+                else cp_async_arrive(full_p + 8 * ps.slot);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Preparation: slots sorted by expert, chunks, the copy of x.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+
+struct SortParams {
+    const int32_t *indices;
+    int slots, E, cap, warps;
+    MoeHeader *hdr;
+    int4 *chunks;
+    int32_t *perm;
+    int *err;
+};
+
+__device__ __forceinline__ int slot_key(const int32_t *indices, int p, int E, int *err) {
+    const int e = moe_expert(indices, p, E, err);
+    return e < 0 ? E : e;
+}
+
+// Exclusive prefix sum of a[0..L) in place, a[L] the total; by the whole block.
+__device__ void scan_counts(int *a, int L, int *tmp) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int per = (L + blockDim.x - 1) / blockDim.x;
+    const int lo = min(L, tid * per), hi = min(L, lo + per);
+    int mine = 0;
+    for (int i = lo; i < hi; ++i) mine += a[i];
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) tmp[warp] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) before += tmp[w];
+        total += tmp[w];
+    }
+    int run = before + incl - mine;
+    for (int i = lo; i < hi; ++i) {
+        const int t = a[i];
+        a[i] = run;
+        run += t;
+    }
+    __syncthreads();
+    if (tid == 0) a[L] = total;
+    __syncthreads();
+}
+
+// Lowest box that holds `rows` rows: its index in kHeights and, above 8 bits, its height.
+__device__ __forceinline__ int box_of(int rows) {
+    if (rows <= 16) return 0 | 16 << 8;
+    if (rows <= 32) return 1 | 32 << 8;
+    if (rows <= 64) return 2 | 64 << 8;
+    if (rows <= 96) return 3 | 96 << 8;
+    if (rows <= 128) return 4 | 128 << 8;
+    return 5 | 192 << 8;
+}
+
+// One CTA: a stable counting sort of the slots by expert (per-warp counts over
+// contiguous stretches, a scan, a scatter ranked within each warp), then each
+// expert's rows cut into near-equal chunks of whole 16 rows, at most cap.
+__global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortParams p) {
+    extern __shared__ int sm[];
+    __shared__ int tmp[32];
+    const int E1 = p.E + 1, W = p.warps;
+    int *cnt = sm, *first = sm + W * E1, *nch = first + E1 + 1;
+    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < W * E1; i += nthr) cnt[i] = 0;
+    __syncthreads();
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int seg = (p.slots + W - 1) / W;
+    const int lo = min(p.slots, warp * seg), hi = min(p.slots, lo + seg);
+    if (warp < W) {
+        for (int b0 = lo; b0 < hi; b0 += 32) {
+            const bool act = b0 + lane < hi;
+            const int key = act ? slot_key(p.indices, b0 + lane, p.E, p.err) : -1 - lane;
+            const unsigned same = __match_any_sync(0xffffffffu, key);
+            if (act && lane == __ffs(same) - 1) cnt[warp * E1 + key] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    for (int k = tid; k < E1; k += nthr) {
+        int run = 0;
+        for (int w = 0; w < W; ++w) {
+            const int t = cnt[w * E1 + k];
+            cnt[w * E1 + k] = run;
+            run += t;
+        }
+        first[k] = run;
+    }
+    __syncthreads();
+    scan_counts(first, E1, tmp);
+    if (warp < W) {
+        const unsigned lt = (1u << lane) - 1u;
+        for (int b0 = lo; b0 < hi; b0 += 32) {
+            const bool act = b0 + lane < hi;
+            const int key = act ? slot_key(p.indices, b0 + lane, p.E, nullptr) : -1 - lane;
+            const unsigned same = __match_any_sync(0xffffffffu, key);
+            int pos = 0;
+            if (act) pos = first[key] + cnt[warp * E1 + key] + __popc(same & lt);
+            __syncwarp();
+            if (act) {
+                p.perm[pos] = b0 + lane;
+                if (lane == __ffs(same) - 1) cnt[warp * E1 + key] += __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+    auto size_of = [&](int rows) {
+        const int n = (rows + p.cap - 1) / p.cap;
+        return min(p.cap, ((rows + n - 1) / n + 15) & ~15);
+    };
+    for (int k = tid; k < p.E; k += nthr) {
+        const int rows = first[k + 1] - first[k];
+        nch[k] = rows ? (rows + size_of(rows) - 1) / size_of(rows) : 0;
+    }
+    __syncthreads();
+    scan_counts(nch, p.E, tmp);
+    for (int k = tid; k < p.E; k += nthr) {
+        const int rows = first[k + 1] - first[k];
+        if (rows == 0) continue;
+        const int size = size_of(rows);
+        for (int j = 0; j * size < rows; ++j) {
+            const int n = min(size, rows - j * size);
+            p.chunks[nch[k] + j] = make_int4(k, first[k] + j * size, n, box_of(n));
+        }
+    }
+    if (tid == 0) {
+        p.hdr->num_chunks = nch[p.E];
+        p.hdr->valid = first[p.E];
+    }
+}
+
+// x rows in sorted order as [K / 64][slots][64], every eight elements in the
+// order 0 4 1 5 2 6 3 7.
+__global__ void __launch_bounds__(256) moe_rows_kernel(const uint4 *x, uint4 *xs, const int32_t *perm,
+                                                       const MoeHeader *hdr, int slots, int top_k, int vec) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int valid = hdr->valid;
+    for (int r = blockIdx.x; r < valid; r += gridDim.x) {
+        const uint4 *src = x + (int64_t)(perm[r] / top_k) * vec;
+        for (int v = threadIdx.x; v < vec; v += blockDim.x) {
+            const uint4 a = __ldg(src + v);
+            xs[((int64_t)(v >> 3) * slots + r) * 8 + (v & 7)] =
+                make_uint4(__byte_perm(a.x, a.z, 0x5410), __byte_perm(a.x, a.z, 0x7632),
+                           __byte_perm(a.y, a.w, 0x5410), __byte_perm(a.y, a.w, 0x7632));
+        }
+    }
+}
+
+// y[t] = sum over slots in order of weight * part, rounded once.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const float *parts, const int32_t *indices,
+                                                          const float *weights, T *y, int64_t total, int N,
+                                                          int top_k, int E) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int nv = N / VEC;
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t t = i / nv;
+        const int n = (int)(i - t * nv) * VEC;
+        float acc[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[c] = 0.f;
+        for (int j = 0; j < top_k; ++j) {
+            const int64_t slot = t * top_k + j;
+            const int e = indices[slot];
+            if (e < 0 || e >= E) continue;
+            const float w = weights[slot];
+            const float *src = parts + slot * N + n;
+            if constexpr (VEC == 4) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(src));
+                acc[0] = __fmaf_rn(w, v.x, acc[0]);
+                acc[1] = __fmaf_rn(w, v.y, acc[1]);
+                acc[2] = __fmaf_rn(w, v.z, acc[2]);
+                acc[3] = __fmaf_rn(w, v.w, acc[3]);
+            } else {
+                acc[0] = __fmaf_rn(w, *src, acc[0]);
+            }
+        }
+        if constexpr (VEC == 4) {
+            *reinterpret_cast<uint2 *>(y + t * N + n) =
+                make_uint2(Half2<T>::pack(acc[0], acc[1]), Half2<T>::pack(acc[2], acc[3]));
+        } else {
+            y[t * N + n] = Dt<T>::from_f(acc[0]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+MoePlan plan_of(const ExpertsArgs &a) {
+    MoePlan w{};
+    const int64_t P = a.T * a.top_k;
+    w.max_chunks = a.n_experts + (P + 15) / 16 + 1;
+    size_t off = 256;
+    w.chunks = off;
+    off += up256((size_t)w.max_chunks * sizeof(int4));
+    w.perm = off;
+    off += up256((size_t)P * 4);
+    w.x = off;
+    off += up256((size_t)P * (size_t)a.K * 2);
+    w.h = off;
+    off += up256((size_t)P * (size_t)a.I * 2);
+    w.parts = off;
+    off += up256((size_t)P * (size_t)a.N * 4);
+    w.total = off;
+    return w;
+}
+
+template <typename F, typename... Args>
+cudaError_t launch_chained(F kern, dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+// Rows per chunk at most: an expert's rows mostly fit one narrow chunk when
+// there are few of them, and the rings hold more packed stages then.
+int chunk_cap(int64_t slots, int64_t E) { return slots <= 32 * E ? 64 : 192; }
+
+template <typename T, int MODE, bool GLU>
+cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStream_t s) {
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    const int64_t P = a.T * a.top_k, C = GLU ? a.K : a.I, R = GLU ? a.I : a.N;
+    constexpr int NM = GLU ? 2 : 1, NW = MODE == QMM_MODE_AFFINE ? 2 : 1;
+    constexpr int ES = MODE == QMM_MODE_AFFINE ? 2 : 1;
+    const ExpertWeight *ew[2] = {GLU ? &a.gate : &a.down, GLU ? &a.up : &a.down};
+    CUtensorMap mw[2];
+    for (int m = 0; m < 2; ++m)
+        if (!make_map_2d(&mw[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, ew[m]->wq, (uint64_t)C / 8,
+                         (uint64_t)(a.n_experts * R), (uint64_t)C / 2, kStageK / 8, kBM / NM,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    TcParams p{};
+    p.BS = 2;
+    ActMaps mb;
+    const uint64_t dims[3] = {64, (uint64_t)P, (uint64_t)C / 64};
+    const uint64_t strides[2] = {128, (uint64_t)P * 128};
+    for (int i = 0; i < kNumHeights; ++i) {
+        const uint32_t box[3] = {64, (uint32_t)kHeights[i], (uint32_t)p.BS};
+        if (!make_map(&mb.m[i], std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      3, ws + (GLU ? w.x : w.h), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
+    for (int m = 0; m < 2; ++m) {
+        p.scales[m] = ew[m]->scales;
+        p.biases[m] = ew[m]->biases;
+    }
+    p.out = ws + (GLU ? w.h : w.parts);
+    p.row_bytes_sb = C / a.group_size * ES;
+    p.sb_vec = p.row_bytes_sb % 16 == 0 ? 16 : (p.row_bytes_sb % 4 == 0 ? 4 : 2);
+    p.rows = (int)P;
+    p.R = (int)R;
+    p.KB = (int)(C / kBK);
+    p.gs_log = a.group_size == 16 ? 4 : (a.group_size == 32 ? 5 : (a.group_size == 64 ? 6 : 7));
+    p.n_tiles = (int)((R + kBM / NM - 1) / (kBM / NM));
+    p.acc_stride = cap <= 128 ? 128 : 192;
+    p.na_log = cap <= 128 ? 3 : 2;
+    p.b_bytes = cap * 128 * p.BS;
+    p.SB = cap <= 64 ? 5 : 3;
+    constexpr size_t kSmemMax = 227 * 1024;
+    const size_t fixed = 1024 + 1024;  // alignment; barriers
+    const size_t p_bytes = kPBytes + NW * kWinBytes;
+    p.SP = (int)std::min<size_t>(8, (kSmemMax - fixed - (size_t)p.SB * p.b_bytes) / p_bytes);
+    if (p.SP < 2) return cudaErrorInvalidConfiguration;
+    const size_t smem = fixed + (size_t)p.SB * p.b_bytes + p.SP * p_bytes;
+    p.act = a.act;
+    p.hdr = reinterpret_cast<const MoeHeader *>(ws + w.hdr);
+    p.chunks = reinterpret_cast<const int4 *>(ws + w.chunks);
+    p.perm = reinterpret_cast<const int32_t *>(ws + w.perm);
+    p.err = device_error_word();
+    auto kern = moe_tc_kernel<T, MODE, GLU>;
+    struct Tag;
+    cudaError_t e = configure_once<Tag>(kSmemMax, [&]() {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t most = std::min<int64_t>(w.max_chunks, std::min<int64_t>(P, a.n_experts) + P / 16) * p.n_tiles;
+    const int grid = (int)std::min<int64_t>(std::max<int64_t>(most, 1), num_sms());
+    return launch_chained(kern, dim3(grid), kThreads, smem, s, mw[0], mw[1], mb, p);
+}
+
+template <typename T, int MODE>
+cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
+    const MoePlan w = plan_of(a);
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    const int64_t P = a.T * a.top_k;
+    const int cap = chunk_cap(P, a.n_experts);
+    MoeHeader *hdr = reinterpret_cast<MoeHeader *>(ws + w.hdr);
+    int32_t *perm = reinterpret_cast<int32_t *>(ws + w.perm);
+
+    SortParams sp{};
+    sp.indices = a.indices;
+    sp.slots = (int)P;
+    sp.E = (int)a.n_experts;
+    sp.cap = cap;
+    sp.hdr = hdr;
+    sp.chunks = reinterpret_cast<int4 *>(ws + w.chunks);
+    sp.perm = perm;
+    sp.err = device_error_word();
+    const int E1 = sp.E + 1;
+    sp.warps = (int)std::min<int64_t>(kSortThreads / 32, (P + 31) / 32);
+    const size_t smem = (size_t)(sp.warps * E1 + 2 * (E1 + 1)) * sizeof(int);
+    struct Tag;
+    cudaError_t e = configure_once<Tag>((size_t)160 * 1024, [&]() {
+        return cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    });
+    if (e != cudaSuccess) return e;
+    if ((e = launch_chained(moe_sort_kernel, dim3(1), kSortThreads, smem, s, sp)) != cudaSuccess) return e;
+
+    const int vec = (int)(a.K / 8);
+    const int rgrid = (int)std::min<int64_t>(P, (int64_t)num_sms() * 8);
+    e = launch_chained(moe_rows_kernel, dim3(rgrid), 256, 0, s, static_cast<const uint4 *>(a.x),
+                       reinterpret_cast<uint4 *>(ws + w.x), (const int32_t *)perm, (const MoeHeader *)hdr, (int)P,
+                       a.top_k, vec);
+    if (e != cudaSuccess) return e;
+    if ((e = run_product<T, MODE, true>(a, w, cap, s)) != cudaSuccess) return e;
+    if ((e = run_product<T, MODE, false>(a, w, cap, s)) != cudaSuccess) return e;
+
+    const float *parts = reinterpret_cast<const float *>(ws + w.parts);
+    const bool vec4 = a.N % 4 == 0;
+    const int64_t total = a.T * (a.N / (vec4 ? 4 : 1));
+    const int cgrid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)num_sms() * 8);
+    T *y = static_cast<T *>(a.y);
+    if (vec4)
+        return launch_chained(moe_combine_kernel<T, 4>, dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
+                              (int)a.N, a.top_k, (int)a.n_experts);
+    return launch_chained(moe_combine_kernel<T, 1>, dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
+                          (int)a.N, a.top_k, (int)a.n_experts);
+}
+
+template <typename T>
+cudaError_t run_tc_mode(const ExpertsArgs &a, cudaStream_t s) {
+    switch (a.mode) {
+    case QMM_MODE_AFFINE: return run_tc<T, QMM_MODE_AFFINE>(a, s);
+    case QMM_MODE_MXFP4: return run_tc<T, QMM_MODE_MXFP4>(a, s);
+    default: return run_tc<T, QMM_MODE_NVFP4>(a, s);
+    }
+}
+
+}  // namespace
+
+bool moe_tc_supported() { return encode_fn() != nullptr; }
+
+size_t moe_tc_workspace(const ExpertsArgs &a) { return plan_of(a).total; }
+
+cudaError_t launch_moe_tc(qmm_dtype dt, const ExpertsArgs &a, cudaStream_t s) {
+    return dt == QMM_BF16 ? run_tc_mode<__nv_bfloat16>(a, s) : run_tc_mode<__half>(a, s);
+}
+
+}  // namespace qmm

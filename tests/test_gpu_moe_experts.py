@@ -11,7 +11,7 @@ from quantized_matmul_03_b200 import binding as qb
 pytestmark = pytest.mark.gpu
 
 MODES = [("mxfp4", 32), ("nvfp4", 16), ("affine", 32), ("affine", 64), ("affine", 128)]
-PATHS = ["gemv"]
+PATHS = ["gemv", "gemm"]
 FEW = ["gemv"]
 
 

@@ -69,6 +69,9 @@ constexpr int kBM = 128, kBK = 64;
 constexpr int kStageK = kBK * kGroups;    // k per packed stage
 constexpr int kPBytes = kBM * kStageK / 2;  // 16 KB
 constexpr int kWinBytes = kBM * 16;       // one window of 16 bytes per row
+constexpr int kPair = 2;                  // k-blocks per hand-over to the MMA
+constexpr int kRing = 8;                  // hand-over barriers (more than pairs in flight)
+constexpr int kBarBytes = 1024;           // barriers and the tensor-memory address
 constexpr int kNumHeights = 6;
 constexpr int kHeights[kNumHeights] = {16, 32, 64, 96, 128, 192};
 
@@ -92,8 +95,8 @@ struct TcParams {
     int64_t row_bytes_sb;     // bytes of one row of scales
     int rows;                 // slots
     int R, KB, gs_log, n_tiles;
-    int acc_stride, na_log;   // columns per accumulator; log2 of A slots
-    int SP, SB, BS, b_bytes;  // ring depths, k-blocks and bytes of an activation stage
+    int acc_stride, na;       // columns per accumulator; pairs of A slots
+    int SP, SB, b_bytes;      // ring depths; bytes of an activation stage (a pair of k-blocks)
     int sb_vec;               // scale copies of 16, 4 or 2 bytes
     int act;
     const MoeHeader *hdr;
@@ -250,6 +253,19 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Bounded wait for a barrier phase.  The polls come first: the clock and the
+// limit, a read of global memory that costs as much as a block's work, are
+// looked at only once a wait has gone on for long.  SLEEP: the thread may be
+// suspended between polls.  On timeout the device error word is set and the
+// caller carries on in bounds.
+template <bool SLEEP = true>
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, int *err) {
+#pragma unroll 1
+    for (int i = 0; i < (SLEEP ? 16 : 4096); ++i)
+        if (SLEEP ? ptx::mbar_try_wait(bar, parity) : ptx::mbar_test(bar, parity)) return;
+    ptx::mbar_wait<true>(bar, parity, err);
+}
+
 struct Ring {
     int slot = 0;
     uint32_t phase = 0;
@@ -276,13 +292,17 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
-    const int SP = p.SP, SB = p.SB, NA = 1 << p.na_log;
-    const uint32_t b0 = base, p0 = b0 + SB * p.b_bytes, s0 = p0 + SP * kPBytes;
-    const uint32_t bars = s0 + SP * NW * kWinBytes;
-    const uint32_t full_p = bars, empty_p = full_p + 8 * SP, full_b = empty_p + 8 * SP, empty_b = full_b + 8 * SB;
-    const uint32_t full_a = empty_b + 8 * SB, empty_a = full_a + 8 * NA;
-    const uint32_t acc_full = empty_a + 8 * NA, acc_empty = acc_full + 16, done = acc_empty + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + (done + 8 - base));
+    const int SP = p.SP, SB = p.SB;
+    const uint32_t NA = p.na;
+    // Barriers first, then the rings: activations, packed tiles, windows.
+    const uint32_t bars = base, b0 = base + kBarBytes, p0 = b0 + SB * p.b_bytes, s0 = p0 + SP * kPBytes;
+    // full_p, empty_p: packed stages.  Pair n of k-blocks (counted over all of
+    // the CTA's tiles) is handed over on ready[n % kRing]: eight dequantize
+    // warps and the activation tile's bytes; its MMAs complete done[n % kRing],
+    // which frees pair slot n % NA of A and activation stage n % SB.
+    const uint32_t full_p = bars, empty_p = full_p + 8 * SP, ready = empty_p + 8 * SP, done = ready + 8 * kRing;
+    const uint32_t acc_full = done + 8 * kRing, acc_empty = acc_full + 16, fin = acc_empty + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + (fin + 8 - base));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -290,19 +310,15 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
             ptx::mbar_init(full_p + 8 * i, NM + 32);
             ptx::mbar_init(empty_p + 8 * i, kDqWarps);
         }
-        for (int i = 0; i < SB; ++i) {
-            ptx::mbar_init(full_b + 8 * i, 1);
-            ptx::mbar_init(empty_b + 8 * i, 1);
-        }
-        for (int i = 0; i < NA; ++i) {
-            ptx::mbar_init(full_a + 8 * i, 4);
-            ptx::mbar_init(empty_a + 8 * i, 1);
+        for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(ready + 8 * i, 4 * kPair + 1);
+            ptx::mbar_init(done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(acc_full + 8 * i, 1);
             ptx::mbar_init(acc_empty + 8 * i, 4);
         }
-        ptx::mbar_init(done, 1);
+        ptx::mbar_init(fin, 1);
         ptx::fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -316,7 +332,7 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
     // What the preceding kernels wrote (chunks, activations) is read from here on.
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int KB = p.KB, KS = (KB + kGroups - 1) / kGroups;
+    const int KB = p.KB, KS = (KB + kGroups - 1) / kGroups, KP = (KB + kPair - 1) / kPair;
     const int num_tiles = p.hdr->num_chunks * p.n_tiles;
     const uint32_t a_col0 = 2u * p.acc_stride;
 
@@ -332,7 +348,7 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
         for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
             for (int st = 0; st < KS; ++st, ps.next(SP)) {
                 const int kb = st * kGroups + g;
-                ptx::mbar_wait(full_p + 8 * ps.slot, ps.phase, p.err);
+                wait_phase(full_p + 8 * ps.slot, ps.phase, p.err);
                 if (kb < KB) {
                     uint32_t w[8], sb = 0, bb = 0;
                     const uint8_t *src = prow + ps.slot * kPBytes;
@@ -362,20 +378,26 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                     dequant_block<T, MODE>(w, sb, bb, v);
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
-                    const uint32_t cc = c + kb, slot = cc & (NA - 1);
-                    if (cc >= (uint32_t)NA) ptx::mbar_wait(empty_a + 8 * slot, ((cc >> p.na_log) & 1) ^ 1, p.err);
+                    const uint32_t n = c + kb / kPair;
+                    if (n >= NA) wait_phase(done + 8 * ((n - NA) % kRing), ((n - NA) / kRing) & 1, p.err);
                     tc_fence_after();
-                    tmem_st32(dst + 32u * slot, v);
+                    tmem_st32(dst + 64u * (n & (NA - 1)) + 32u * (kb & 1), v);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(full_a + 8 * slot);
+                    if (lane == 0) ptx::mbar_arrive(ready + 8 * (n % kRing));
                 } else {
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
+                    if (kb == KB && (kb & 1)) {  // the missing half of the tile's last pair
+                        const uint32_t n = c + kb / kPair;
+                        if (n >= NA) wait_phase(done + 8 * ((n - NA) % kRing), ((n - NA) / kRing) & 1, p.err);
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(ready + 8 * (n % kRing));
+                    }
                 }
             }
-            c += KB;
+            c += KP;
         }
     } else if (warp < kMmaWarp) {
         // ------------------------- epilogue -------------------------
@@ -385,7 +407,7 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
             const int acc = i & 1, use = i >> 1;
             const int4 ch = p.chunks[tile / p.n_tiles];
             const int nt = tile % p.n_tiles;
-            ptx::mbar_wait(acc_full + 8 * acc, use & 1, p.err);
+            wait_phase(acc_full + 8 * acc, use & 1, p.err);
             tc_fence_after();
             const int nj = (ch.z + 31) / 32;
             for (int j = 0; j < nj; ++j) {
@@ -428,51 +450,46 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
         }
     } else if (warp == kMmaWarp) {
         // ------------------------- MMA issuer -------------------------
-        const bool leader = elect_one();
-        uint32_t c = 0;
-        int i = 0;
-        Ring bs;
-        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++i) {
-            const int acc = i & 1, use = i >> 1;
-            const int4 ch = p.chunks[tile / p.n_tiles];
-            const uint32_t idesc = make_idesc(kF16, kBM, (ch.z + 15) & ~15);
-            const uint32_t zbytes = (uint32_t)(ch.w >> 8) * 128u;  // one k-block of the activation tile
-            if (leader && i >= 2) ptx::mbar_wait(acc_empty + 8 * acc, (use + 1) & 1, p.err);
-            __syncwarp();
-            tc_fence_after();
-            const uint32_t d = tmem + acc * p.acc_stride;
-            int kz = 0;
-            for (int kb = 0; kb < KB; ++kb) {
-                const uint32_t cc = c + kb, slot = cc & (NA - 1);
-                const bool last = kz == p.BS - 1 || kb == KB - 1;
-                if (leader) {
-                    if (kz == 0) ptx::mbar_wait<false>(full_b + 8 * bs.slot, bs.phase, p.err);
-                    ptx::mbar_wait<false>(full_a + 8 * slot, (cc >> p.na_log) & 1, p.err);
+        // One elected lane runs the whole loop: with the loop shared by the warp
+        // and only the waits and issues under the election, the commit of a tile
+        // that had waited long for its accumulator went to the other
+        // accumulator's barrier.
+        if (elect_one()) {
+            uint32_t n = 0;
+            int i = 0, bslot = 0;
+            for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++i) {
+                const int acc = i & 1, use = i >> 1;
+                const int4 ch = p.chunks[tile / p.n_tiles];
+                const uint32_t idesc = make_idesc(kF16, kBM, (ch.z + 15) & ~15);
+                const uint32_t zstep = (uint32_t)(ch.w >> 8) * 128u >> 4;  // descriptor step of one k-block
+                if (i >= 2) wait_phase<false>(acc_empty + 8 * acc, (use + 1) & 1, p.err);
+                tc_fence_after();
+                const uint32_t d = tmem + acc * p.acc_stride;
+                for (int kp = 0; kp < KP; ++kp, ++n) {
+                    wait_phase<false>(ready + 8 * (n % kRing), (n / kRing) & 1, p.err);
                     tc_fence_after();
-                    const uint64_t db = sw128_desc(b0 + bs.slot * p.b_bytes + kz * zbytes);
-                    const uint32_t ta = tmem + a_col0 + 32u * slot;
-                    tc_mma_ts(d, ta, db, idesc, kb != 0);
+                    uint64_t db = sw128_desc(b0 + bslot * p.b_bytes);
+                    uint32_t ta = tmem + a_col0 + 64u * (n & (NA - 1));
+                    tc_mma_ts(d, ta, db, idesc, kp != 0);
                     tc_mma_ts(d, ta + 8, db + 2, idesc, 1);
                     tc_mma_ts(d, ta + 16, db + 4, idesc, 1);
                     tc_mma_ts(d, ta + 24, db + 6, idesc, 1);
-                    tc_commit(empty_a + 8 * slot);
-                    if (last) tc_commit(empty_b + 8 * bs.slot);
+                    if (2 * kp + 1 < KB) {
+                        db += zstep;
+                        ta += 32;
+                        tc_mma_ts(d, ta, db, idesc, 1);
+                        tc_mma_ts(d, ta + 8, db + 2, idesc, 1);
+                        tc_mma_ts(d, ta + 16, db + 4, idesc, 1);
+                        tc_mma_ts(d, ta + 24, db + 6, idesc, 1);
+                    }
+                    tc_commit(done + 8 * (n % kRing));
+                    if (++bslot == SB) bslot = 0;
                 }
-                __syncwarp();
-                ++kz;
-                if (last) {
-                    kz = 0;
-                    bs.next(SB);
-                }
+                tc_commit(acc_full + 8 * acc);
             }
-            c += KB;
-            if (leader) tc_commit(acc_full + 8 * acc);
-            __syncwarp();
-        }
-        // Every MMA has completed before tensor memory is freed.
-        if (leader) {
-            tc_commit(done);
-            ptx::mbar_drain(done, 0, p.err);
+            // Every MMA has completed before tensor memory is freed.
+            tc_commit(fin);
+            ptx::mbar_drain(fin, 0, p.err);
         }
         __syncwarp();
     } else if (warp < kBWarp) {
@@ -487,7 +504,7 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                 const int4 ch = p.chunks[tile / p.n_tiles];
                 const int r0 = ch.x * p.R + (tile % p.n_tiles) * (kBM / NM);
                 for (int st = 0; st < KS; ++st, ++n, ps.next(SP)) {
-                    if (ps.wrapped) ptx::mbar_wait(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
+                    if (ps.wrapped) wait_phase(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
                     ptx::mbar_arrive_expect_tx(full_p + 8 * ps.slot, bytes);
                     tma_load_2d(p0 + ps.slot * kPBytes + m * bytes, map, st * (kStageK / 8), r0,
                                 full_p + 8 * ps.slot);
@@ -500,19 +517,21 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
         if (lane == 0) {
             // the activations were written by ordinary stores of earlier kernels
             asm volatile("fence.proxy.async.global;" ::: "memory");
-            Ring bs;
-            int n = 0;
+            uint32_t n = 0;
+            int slot = 0;
             for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
                 const int4 ch = p.chunks[tile / p.n_tiles];
                 const CUtensorMap *map = &map_b.m[ch.w & 255];
-                const uint32_t bytes = (uint32_t)(ch.w >> 8) * 128u * p.BS;
-                for (int kb = 0; kb < KB; kb += p.BS, ++n, bs.next(SB)) {
-                    if (bs.wrapped) ptx::mbar_wait(empty_b + 8 * bs.slot, bs.phase ^ 1, p.err);
-                    ptx::mbar_arrive_expect_tx(full_b + 8 * bs.slot, bytes);
-                    tma_load_3d(b0 + bs.slot * p.b_bytes, map, 0, ch.y, kb, full_b + 8 * bs.slot);
+                const uint32_t bytes = (uint32_t)(ch.w >> 8) * 128u * kPair;
+                for (int kp = 0; kp < KP; ++kp, ++n) {
+                    if (n >= (uint32_t)SB) wait_phase(done + 8 * ((n - SB) % kRing), ((n - SB) / kRing) & 1, p.err);
+                    ptx::mbar_arrive_expect_tx(ready + 8 * (n % kRing), bytes);
+                    tma_load_3d(b0 + slot * p.b_bytes, map, 0, ch.y, kPair * kp, ready + 8 * (n % kRing));
+                    if (++slot == SB) slot = 0;
                 }
             }
-            for (int k = max(0, n - SB); k < n; ++k) ptx::mbar_drain(full_b + 8 * (k % SB), (k / SB) & 1, p.err);
+            for (uint32_t k = n < (uint32_t)SB ? 0 : n - SB; k < n; ++k)
+                ptx::mbar_drain(ready + 8 * (k % kRing), (k / kRing) & 1, p.err);
         }
     } else {
         // ------------------------- scale windows -------------------------
@@ -534,7 +553,7 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                 if constexpr (AFF) src[i][1] = static_cast<const uint8_t *>(p.biases[m]) + off;
             }
             for (int st = 0; st < KS; ++st, ps.next(SP)) {
-                if (ps.wrapped) ptx::mbar_wait(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
+                if (ps.wrapped) wait_phase(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
                 const uint32_t win = s0 + ps.slot * (NW * kWinBytes) + lane * 16;
                 const int64_t at = (((int64_t)st * kStageK) >> p.gs_log) * ES & ~15;  // window's first byte
                 const int left = (int)min((int64_t)16, p.row_bytes_sb - at);
@@ -786,8 +805,8 @@ MoePlan plan_of(const ExpertsArgs &a) {
     return w;
 }
 
-template <typename F, typename... Args>
-cudaError_t launch_chained(F kern, dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+template <auto KERN, typename... Args>
+cudaError_t launch_chained(dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads, 1, 1);
@@ -798,7 +817,7 @@ cudaError_t launch_chained(F kern, dim3 grid, int threads, size_t smem, cudaStre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, KERN, args...);
     if (e != cudaSuccess) return e;
     count_launches(1);
     return cudaGetLastError();
@@ -822,12 +841,11 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStr
                          CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     TcParams p{};
-    p.BS = 2;
     ActMaps mb;
     const uint64_t dims[3] = {64, (uint64_t)P, (uint64_t)C / 64};
     const uint64_t strides[2] = {128, (uint64_t)P * 128};
     for (int i = 0; i < kNumHeights; ++i) {
-        const uint32_t box[3] = {64, (uint32_t)kHeights[i], (uint32_t)p.BS};
+        const uint32_t box[3] = {64, (uint32_t)kHeights[i], kPair};
         if (!make_map(&mb.m[i], std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                       3, ws + (GLU ? w.x : w.h), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -846,11 +864,11 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStr
     p.gs_log = a.group_size == 16 ? 4 : (a.group_size == 32 ? 5 : (a.group_size == 64 ? 6 : 7));
     p.n_tiles = (int)((R + kBM / NM - 1) / (kBM / NM));
     p.acc_stride = cap <= 128 ? 128 : 192;
-    p.na_log = cap <= 128 ? 3 : 2;
-    p.b_bytes = cap * 128 * p.BS;
+    p.na = cap <= 128 ? 4 : 2;
+    p.b_bytes = cap * 128 * kPair;
     p.SB = cap <= 64 ? 5 : 3;
     constexpr size_t kSmemMax = 227 * 1024;
-    const size_t fixed = 1024 + 1024;  // alignment; barriers
+    const size_t fixed = 1024 + kBarBytes;  // alignment; barriers
     const size_t p_bytes = kPBytes + NW * kWinBytes;
     p.SP = (int)std::min<size_t>(8, (kSmemMax - fixed - (size_t)p.SB * p.b_bytes) / p_bytes);
     if (p.SP < 2) return cudaErrorInvalidConfiguration;
@@ -868,7 +886,7 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStr
     if (e != cudaSuccess) return e;
     const int64_t most = std::min<int64_t>(w.max_chunks, std::min<int64_t>(P, a.n_experts) + P / 16) * p.n_tiles;
     const int grid = (int)std::min<int64_t>(std::max<int64_t>(most, 1), num_sms());
-    return launch_chained(kern, dim3(grid), kThreads, smem, s, mw[0], mw[1], mb, p);
+    return launch_chained<moe_tc_kernel<T, MODE, GLU>>(dim3(grid), kThreads, smem, s, mw[0], mw[1], mb, p);
 }
 
 template <typename T, int MODE>
@@ -897,11 +915,11 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
         return cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     });
     if (e != cudaSuccess) return e;
-    if ((e = launch_chained(moe_sort_kernel, dim3(1), kSortThreads, smem, s, sp)) != cudaSuccess) return e;
+    if ((e = launch_chained<moe_sort_kernel>(dim3(1), kSortThreads, smem, s, sp)) != cudaSuccess) return e;
 
     const int vec = (int)(a.K / 8);
     const int rgrid = (int)std::min<int64_t>(P, (int64_t)num_sms() * 8);
-    e = launch_chained(moe_rows_kernel, dim3(rgrid), 256, 0, s, static_cast<const uint4 *>(a.x),
+    e = launch_chained<moe_rows_kernel>(dim3(rgrid), 256, 0, s, static_cast<const uint4 *>(a.x),
                        reinterpret_cast<uint4 *>(ws + w.x), (const int32_t *)perm, (const MoeHeader *)hdr, (int)P,
                        a.top_k, vec);
     if (e != cudaSuccess) return e;
@@ -914,9 +932,9 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
     const int cgrid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)num_sms() * 8);
     T *y = static_cast<T *>(a.y);
     if (vec4)
-        return launch_chained(moe_combine_kernel<T, 4>, dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
+        return launch_chained<moe_combine_kernel<T, 4>>(dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
                               (int)a.N, a.top_k, (int)a.n_experts);
-    return launch_chained(moe_combine_kernel<T, 1>, dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
+    return launch_chained<moe_combine_kernel<T, 1>>(dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
                           (int)a.N, a.top_k, (int)a.n_experts);
 }
 

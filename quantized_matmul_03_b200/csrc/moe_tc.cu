@@ -3,8 +3,8 @@
 //   y[t] = sum_j weights[t, j] (h[t, j] Wd[e]^T)
 //
 // Kernels of one call:
-//   1. prep      slots ordered by expert (stable), each expert's rows cut into
-//                chunks of at most `cap` rows, and x copied into that order;
+//   1. prep      slots ordered by expert (stable), x copied into that order,
+//                each expert's rows cut into chunks of at most `cap` rows;
 //   2. gate/up   grouped product with the gated activation in its epilogue;
 //   3. down      grouped product, one fp32 row per slot;
 //   4. combine   a token's rows added in slot order with their weights and
@@ -147,22 +147,32 @@ __device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+__device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
 // Codes e and e + 4 of w as 2^-126 (bf16) or 2^-14 (f16) times their values.
+// A multiplication moves bits on the FMA pipe, which is idle here, while
+// shifts would go to the integer pipe that the masks already fill.  bf16: a
+// nibble times 2^12 + 2^6 puts its sign at bit 15 and its magnitude at bits
+// 6..8 (the two copies do not overlap, the rest is masked off).  f16, whose
+// copies would overlap: sign and magnitude apart.
 template <typename T>
 __device__ __forceinline__ void e2m1_place(uint32_t w, uint32_t (&r)[4]) {
-    constexpr uint32_t S = 0x80008000u;
+    const uint32_t u = w >> 8;
     if constexpr (std::is_same<T, __half>::value) {
-        constexpr uint32_t M = 0x0E000E00u;
-        r[0] = ((w << 12) & S) | ((w << 9) & M);
-        r[1] = ((w << 8) & S) | ((w << 5) & M);
-        r[2] = ((w << 4) & S) | ((w << 1) & M);
-        r[3] = (w & S) | ((w >> 3) & M);
+        r[0] = mad(w & 0x00070007u, 512u, (w & 0x00080008u) * 4096u);
+        r[1] = mad(w & 0x00700070u, 32u, (w & 0x00800080u) * 256u);
+        r[2] = mad(u & 0x00070007u, 512u, (u & 0x00080008u) * 4096u);
+        r[3] = mad(u & 0x00700070u, 32u, (u & 0x00800080u) * 256u);
     } else {
-        constexpr uint32_t M = 0x01C001C0u;
-        r[0] = ((w << 12) & S) | ((w << 6) & M);
-        r[1] = ((w << 8) & S) | ((w << 2) & M);
-        r[2] = ((w << 4) & S) | ((w >> 2) & M);
-        r[3] = (w & S) | ((w >> 6) & M);
+        constexpr uint32_t M = 0x81C081C0u;
+        r[0] = mad(w & 0x000F000Fu, 4160u, 0u) & M;
+        r[1] = mad(w & 0x00F000F0u, 260u, 0u) & M;
+        r[2] = mad(u & 0x000F000Fu, 4160u, 0u) & M;
+        r[3] = mad(u & 0x00F000F0u, 260u, 0u) & M;
     }
 }
 
@@ -255,14 +265,12 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 
 // Bounded wait for a barrier phase.  The polls come first: the clock and the
 // limit, a read of global memory that costs as much as a block's work, are
-// looked at only once a wait has gone on for long.  SLEEP: the thread may be
-// suspended between polls.  On timeout the device error word is set and the
-// caller carries on in bounds.
-template <bool SLEEP = true>
+// looked at only once a wait has gone on for long.  On timeout the device error
+// word is set and the caller carries on in bounds.
 __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, int *err) {
 #pragma unroll 1
-    for (int i = 0; i < (SLEEP ? 16 : 4096); ++i)
-        if (SLEEP ? ptx::mbar_try_wait(bar, parity) : ptx::mbar_test(bar, parity)) return;
+    for (int i = 0; i < 16; ++i)
+        if (ptx::mbar_try_wait(bar, parity)) return;
     ptx::mbar_wait<true>(bar, parity, err);
 }
 
@@ -462,11 +470,11 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                 const int4 ch = p.chunks[tile / p.n_tiles];
                 const uint32_t idesc = make_idesc(kF16, kBM, (ch.z + 15) & ~15);
                 const uint32_t zstep = (uint32_t)(ch.w >> 8) * 128u >> 4;  // descriptor step of one k-block
-                if (i >= 2) wait_phase<false>(acc_empty + 8 * acc, (use + 1) & 1, p.err);
+                if (i >= 2) wait_phase(acc_empty + 8 * acc, (use + 1) & 1, p.err);
                 tc_fence_after();
                 const uint32_t d = tmem + acc * p.acc_stride;
                 for (int kp = 0; kp < KP; ++kp, ++n) {
-                    wait_phase<false>(ready + 8 * (n % kRing), (n / kRing) & 1, p.err);
+                    wait_phase(ready + 8 * (n % kRing), (n / kRing) & 1, p.err);
                     tc_fence_after();
                     uint64_t db = sw128_desc(b0 + bslot * p.b_bytes);
                     uint32_t ta = tmem + a_col0 + 64u * (n & (NA - 1));
@@ -590,21 +598,19 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
 // ---------------------------------------------------------------------------
 // Preparation: slots sorted by expert, chunks, the copy of x.
 // ---------------------------------------------------------------------------
-constexpr int kSortThreads = 1024;
+constexpr int kPrepThreads = 512, kPrepWarps = kPrepThreads / 32;
+constexpr int kPrepSeg = 256;  // slots of a CTA at most
 
-struct SortParams {
+struct PrepParams {
     const int32_t *indices;
-    int slots, E, cap, warps;
+    const uint4 *x;
+    uint4 *xs;
+    int slots, E, cap, seg, top_k, vec;  // vec: 16-byte units of a row of x
     MoeHeader *hdr;
     int4 *chunks;
     int32_t *perm;
     int *err;
 };
-
-__device__ __forceinline__ int slot_key(const int32_t *indices, int p, int E, int *err) {
-    const int e = moe_expert(indices, p, E, err);
-    return e < 0 ? E : e;
-}
 
 // Exclusive prefix sum of a[0..L) in place, a[L] the total; by the whole block.
 __device__ void scan_counts(int *a, int L, int *tmp) {
@@ -647,69 +653,102 @@ __device__ __forceinline__ int box_of(int rows) {
     return 5 | 192 << 8;
 }
 
-// One CTA: a stable counting sort of the slots by expert (per-warp counts over
-// contiguous stretches, a scan, a scatter ranked within each warp), then each
-// expert's rows cut into near-equal chunks of whole 16 rows, at most cap.
-__global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortParams p) {
+// Each CTA counts every slot's expert for itself (the indices are small and
+// come from L2), which gives it, without a second kernel, where the slots of its
+// own stretch go: the experts' first rows, plus the same expert's slots in
+// earlier stretches, plus the rank within its own.  It then copies their rows
+// of x there, every eight elements in the order 0 4 1 5 2 6 3 7.  The first CTA also cuts each expert's rows into near-equal
+// chunks of whole 16 rows, at most cap.  Counts are integers, and ranks follow
+// the slots' order, so the result does not depend on timing.
+__global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const PrepParams p) {
     extern __shared__ int sm[];
-    __shared__ int tmp[32];
-    const int E1 = p.E + 1, W = p.warps;
-    int *cnt = sm, *first = sm + W * E1, *nch = first + E1 + 1;
-    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    for (int i = tid; i < W * E1; i += nthr) cnt[i] = 0;
+    __shared__ int tmp[kPrepWarps];
+    __shared__ int dst[kPrepSeg];  // sorted row of each slot of the stretch, -1 without an expert
+    const int E = p.E;
+    int *first = sm, *before = first + E + 2, *nch = before + E + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < 2 * E + 3; i += kPrepThreads) sm[i] = 0;
     __syncthreads();
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int seg = (p.slots + W - 1) / W;
-    const int lo = min(p.slots, warp * seg), hi = min(p.slots, lo + seg);
-    if (warp < W) {
-        for (int b0 = lo; b0 < hi; b0 += 32) {
-            const bool act = b0 + lane < hi;
-            const int key = act ? slot_key(p.indices, b0 + lane, p.E, p.err) : -1 - lane;
-            const unsigned same = __match_any_sync(0xffffffffu, key);
-            if (act && lane == __ffs(same) - 1) cnt[warp * E1 + key] += __popc(same);
-            __syncwarp();
+    const int lo = blockIdx.x * p.seg, hi = min(p.slots, lo + p.seg);
+    // Lanes with the same expert add once, for the slots before the stretch and
+    // for all.
+    constexpr int U = 8;  // loads in flight per lane
+    for (int b0 = warp * 32; b0 < p.slots; b0 += U * kPrepThreads) {
+        int key[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = b0 + u * kPrepThreads + lane;
+            key[u] = i < p.slots ? p.indices[i] : INT32_MIN;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int b = b0 + u * kPrepThreads, i = b + lane;
+            if (b >= p.slots) break;
+            const bool in = i < p.slots;
+            if (in && (key[u] < 0 || key[u] >= E)) {
+                if (key[u] != -1 && blockIdx.x == 0) record_device_error(p.err, QMM_ERR_INDEX);
+                key[u] = E;
+            }
+            if (!in) key[u] = -1 - lane;
+            const unsigned same = __match_any_sync(0xffffffffu, key[u]);
+            const unsigned early = __ballot_sync(0xffffffffu, i < lo);
+            if (in && lane == __ffs(same) - 1) {
+                atomicAdd(&first[key[u]], __popc(same));
+                if (same & early) atomicAdd(&before[key[u]], __popc(same & early));
+            }
         }
     }
     __syncthreads();
-    for (int k = tid; k < E1; k += nthr) {
-        int run = 0;
-        for (int w = 0; w < W; ++w) {
-            const int t = cnt[w * E1 + k];
-            cnt[w * E1 + k] = run;
-            run += t;
-        }
-        first[k] = run;
-    }
-    __syncthreads();
-    scan_counts(first, E1, tmp);
-    if (warp < W) {
+    scan_counts(first, E + 1, tmp);
+    if (warp == 0) {
         const unsigned lt = (1u << lane) - 1u;
-        for (int b0 = lo; b0 < hi; b0 += 32) {
-            const bool act = b0 + lane < hi;
-            const int key = act ? slot_key(p.indices, b0 + lane, p.E, nullptr) : -1 - lane;
+        for (int b = lo; b < hi; b += 32) {
+            const int i = b + lane;
+            int key = -1 - lane;
+            if (i < hi) {
+                const int e = moe_expert(p.indices, i, E, nullptr);
+                key = e < 0 ? E : e;
+            }
             const unsigned same = __match_any_sync(0xffffffffu, key);
             int pos = 0;
-            if (act) pos = first[key] + cnt[warp * E1 + key] + __popc(same & lt);
+            if (key >= 0) pos = first[key] + before[key] + __popc(same & lt);
             __syncwarp();
-            if (act) {
-                p.perm[pos] = b0 + lane;
-                if (lane == __ffs(same) - 1) cnt[warp * E1 + key] += __popc(same);
+            if (key >= 0) {
+                if (lane == __ffs(same) - 1) before[key] += __popc(same);
+                dst[i - lo] = key < E ? pos : -1;
+                if (key < E) p.perm[pos] = i;
             }
             __syncwarp();
         }
     }
+    __syncthreads();
+    for (int j = warp; j < hi - lo; j += kPrepWarps) {
+        const int r = dst[j];
+        if (r < 0) continue;
+        const uint4 *src = p.x + (int64_t)((lo + j) / p.top_k) * p.vec;
+        uint4 *out = p.xs + (int64_t)r * p.vec;
+#pragma unroll 4
+        for (int v = lane; v < p.vec; v += 32) {
+            const uint4 a = __ldg(src + v);
+            out[v] =
+                make_uint4(__byte_perm(a.x, a.z, 0x5410), __byte_perm(a.x, a.z, 0x7632),
+                           __byte_perm(a.y, a.w, 0x5410), __byte_perm(a.y, a.w, 0x7632));
+        }
+    }
+    if (blockIdx.x != 0) return;
     auto size_of = [&](int rows) {
         const int n = (rows + p.cap - 1) / p.cap;
         return min(p.cap, ((rows + n - 1) / n + 15) & ~15);
     };
-    for (int k = tid; k < p.E; k += nthr) {
+    for (int k = tid; k < E; k += kPrepThreads) {
         const int rows = first[k + 1] - first[k];
         nch[k] = rows ? (rows + size_of(rows) - 1) / size_of(rows) : 0;
     }
     __syncthreads();
-    scan_counts(nch, p.E, tmp);
-    for (int k = tid; k < p.E; k += nthr) {
+    scan_counts(nch, E, tmp);
+    for (int k = tid; k < E; k += kPrepThreads) {
         const int rows = first[k + 1] - first[k];
         if (rows == 0) continue;
         const int size = size_of(rows);
@@ -719,26 +758,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) moe_sort_kernel(const SortPar
         }
     }
     if (tid == 0) {
-        p.hdr->num_chunks = nch[p.E];
-        p.hdr->valid = first[p.E];
-    }
-}
-
-// x rows in sorted order as [K / 64][slots][64], every eight elements in the
-// order 0 4 1 5 2 6 3 7.
-__global__ void __launch_bounds__(256) moe_rows_kernel(const uint4 *x, uint4 *xs, const int32_t *perm,
-                                                       const MoeHeader *hdr, int slots, int top_k, int vec) {
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
-    const int valid = hdr->valid;
-    for (int r = blockIdx.x; r < valid; r += gridDim.x) {
-        const uint4 *src = x + (int64_t)(perm[r] / top_k) * vec;
-        for (int v = threadIdx.x; v < vec; v += blockDim.x) {
-            const uint4 a = __ldg(src + v);
-            xs[((int64_t)(v >> 3) * slots + r) * 8 + (v & 7)] =
-                make_uint4(__byte_perm(a.x, a.z, 0x5410), __byte_perm(a.x, a.z, 0x7632),
-                           __byte_perm(a.y, a.w, 0x5410), __byte_perm(a.y, a.w, 0x7632));
-        }
+        p.hdr->num_chunks = nch[E];
+        p.hdr->valid = first[E];
     }
 }
 
@@ -843,7 +864,8 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStr
     TcParams p{};
     ActMaps mb;
     const uint64_t dims[3] = {64, (uint64_t)P, (uint64_t)C / 64};
-    const uint64_t strides[2] = {128, (uint64_t)P * 128};
+    // x rows as they are ([slots][K], k-blocks 128 bytes apart); h by k-blocks
+    const uint64_t strides[2] = {GLU ? (uint64_t)C * 2 : 128, GLU ? 128 : (uint64_t)P * 128};
     for (int i = 0; i < kNumHeights; ++i) {
         const uint32_t box[3] = {64, (uint32_t)kHeights[i], kPair};
         if (!make_map(&mb.m[i], std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
@@ -898,30 +920,24 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
     MoeHeader *hdr = reinterpret_cast<MoeHeader *>(ws + w.hdr);
     int32_t *perm = reinterpret_cast<int32_t *>(ws + w.perm);
 
-    SortParams sp{};
-    sp.indices = a.indices;
-    sp.slots = (int)P;
-    sp.E = (int)a.n_experts;
-    sp.cap = cap;
-    sp.hdr = hdr;
-    sp.chunks = reinterpret_cast<int4 *>(ws + w.chunks);
-    sp.perm = perm;
-    sp.err = device_error_word();
-    const int E1 = sp.E + 1;
-    sp.warps = (int)std::min<int64_t>(kSortThreads / 32, (P + 31) / 32);
-    const size_t smem = (size_t)(sp.warps * E1 + 2 * (E1 + 1)) * sizeof(int);
-    struct Tag;
-    cudaError_t e = configure_once<Tag>((size_t)160 * 1024, [&]() {
-        return cudaFuncSetAttribute(moe_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    });
-    if (e != cudaSuccess) return e;
-    if ((e = launch_chained<moe_sort_kernel>(dim3(1), kSortThreads, smem, s, sp)) != cudaSuccess) return e;
-
-    const int vec = (int)(a.K / 8);
-    const int rgrid = (int)std::min<int64_t>(P, (int64_t)num_sms() * 8);
-    e = launch_chained<moe_rows_kernel>(dim3(rgrid), 256, 0, s, static_cast<const uint4 *>(a.x),
-                       reinterpret_cast<uint4 *>(ws + w.x), (const int32_t *)perm, (const MoeHeader *)hdr, (int)P,
-                       a.top_k, vec);
+    PrepParams pp{};
+    pp.indices = a.indices;
+    pp.x = static_cast<const uint4 *>(a.x);
+    pp.xs = reinterpret_cast<uint4 *>(ws + w.x);
+    pp.slots = (int)P;
+    pp.E = (int)a.n_experts;
+    pp.cap = cap;
+    pp.top_k = a.top_k;
+    pp.vec = (int)(a.K / 8);
+    pp.hdr = hdr;
+    pp.chunks = reinterpret_cast<int4 *>(ws + w.chunks);
+    pp.perm = perm;
+    pp.err = device_error_word();
+    // Two CTAs per SM, unless their stretches would be shorter than a warp's
+    // share of rows or longer than shared memory holds.
+    pp.seg = (int)std::min<int64_t>(kPrepSeg, std::max<int64_t>(8, (P + 2 * num_sms() - 1) / (2 * num_sms())));
+    const size_t smem = (size_t)(3 * (pp.E + 2)) * sizeof(int);
+    cudaError_t e = launch_chained<moe_prep_kernel>(dim3((unsigned)((P + pp.seg - 1) / pp.seg)), kPrepThreads, smem, s, pp);
     if (e != cudaSuccess) return e;
     if ((e = run_product<T, MODE, true>(a, w, cap, s)) != cudaSuccess) return e;
     if ((e = run_product<T, MODE, false>(a, w, cap, s)) != cudaSuccess) return e;

@@ -222,6 +222,39 @@ __device__ __forceinline__ float reduce8(float (&v)[8], int lane) {
     return r;
 }
 
+// From the partial sums of a CTA's rows: h, or the tokens' outputs.
+template <typename T, bool GLU>
+__device__ __forceinline__ void finish_rows(const GemvParams &p, const float *part, int64_t r0, int nr) {
+    if constexpr (GLU) {
+        float *h = static_cast<float *>(p.out);
+        for (int i = threadIdx.x; i < p.P * nr; i += blockDim.x) {
+            const int slot = i / nr, r = i - slot * nr;
+            if (moe_expert(p.indices, slot, p.E, nullptr) < 0) continue;
+            float g = 0.f, up = 0.f;
+            for (int s = 0; s < p.S; ++s) {
+                const float *q = part + ((int64_t)(slot * p.S + s) * p.rows_cta + r) * 2;
+                g += q[0];
+                up += q[1];
+            }
+            h[(int64_t)slot * p.R + r0 + r] = moe_gate(g, p.act) * up;
+        }
+    } else {
+        const int T_ = p.P / p.top_k;
+        for (int i = threadIdx.x; i < T_ * nr; i += blockDim.x) {
+            const int t = i / nr, r = i - t * nr;
+            float acc = 0.f;
+            for (int j = 0; j < p.top_k; ++j) {
+                const int slot = t * p.top_k + j;
+                if (moe_expert(p.indices, slot, p.E, nullptr) < 0) continue;
+                float d = 0.f;
+                for (int s = 0; s < p.S; ++s) d += part[(int64_t)(slot * p.S + s) * p.rows_cta + r];
+                acc = __fmaf_rn(__ldg(p.weights + slot), d, acc);
+            }
+            static_cast<T *>(p.out)[(int64_t)t * p.R + r0 + r] = Dt<T>::from_f(acc);
+        }
+    }
+}
+
 // X: type of the activations (T, or float for h).  GLU: the first kernel.
 template <typename T, typename X, int MODE, bool GLU>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1) moe_gemv_kernel(const GemvParams p) {
@@ -307,39 +340,216 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) moe_gemv_kernel(const GemvP
         }
     }
     __syncthreads();
-    if constexpr (GLU) {
-        float *h = static_cast<float *>(p.out);
-        for (int i = threadIdx.x; i < p.P * nr; i += blockDim.x) {
-            const int slot = i / nr, r = i - slot * nr;
-            if (moe_expert(p.indices, slot, p.E, nullptr) < 0) continue;
-            float g = 0.f, up = 0.f;
-            for (int s = 0; s < p.S; ++s) {
-                const float *q = part + ((int64_t)(slot * p.S + s) * p.rows_cta + r) * 2;
-                g += q[0];
-                up += q[1];
-            }
-            h[(int64_t)slot * p.R + r0 + r] = moe_gate(g, p.act) * up;
+    finish_rows<T, GLU>(p, part, r0, nr);
+}
+
+// ---------------------------------------------------------------------------
+// The streaming form: the same units and arithmetic, with the weights brought
+// in by bulk copies.  CTA c's rows of a slot's expert are one contiguous
+// stretch of codes and one of scales; a producer warp streams them, a few rows
+// of every slot of a round at a time, through a ring of stages in shared memory,
+// so that the copies in flight depend on neither registers nor the warps'
+// progress.  A round is as many slots as 16 consumer warps have units for; with
+// few units a stage's rows are split among them.  The second kernel starts its
+// copies before the first has finished: it waits only with its activations.
+// ---------------------------------------------------------------------------
+struct StreamParams {
+    GemvParams g;
+    int slots_round, rounds, rows_stage, stages, stage_bytes;
+    int row_bytes, sb_bytes;  // of one row: codes; scales (or biases)
+};
+
+template <typename T, typename X, int MODE, bool GLU>
+__global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) moe_stream_kernel(const StreamParams sp) {
+    constexpr int NM = GLU ? 2 : 1;
+    constexpr bool AFF = MODE == QMM_MODE_AFFINE;
+    constexpr int NA = AFF ? 3 : 2;       // arrays per matrix: codes, scales (, biases)
+    constexpr int RB = kLoads / NM;       // rows of a warp per stage at most
+    extern __shared__ __align__(128) uint8_t sm[];
+    const GemvParams &p = sp.g;
+    const int D = sp.stages;
+    const uint32_t full = ptx::smem_addr(sm), empty = full + 8 * D;
+    uint8_t *ring = sm + 128;
+    float *part = reinterpret_cast<float *>(ring + (size_t)D * sp.stage_bytes);  // [slot][seg][row][NM]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r0 = (int64_t)blockIdx.x * p.rows_cta;
+    const int nr = (int)min((int64_t)p.rows_cta, p.R - r0);
+    const int nst = (nr + sp.rows_stage - 1) / sp.rows_stage;  // stages of a round
+    // Bytes of one slot and matrix in a stage: codes, scales, biases of rows_stage rows.
+    const int mat_bytes = sp.rows_stage * (sp.row_bytes + (NA - 1) * sp.sb_bytes);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < D; ++i) {
+            ptx::mbar_init(full + 8 * i, 1);
+            ptx::mbar_init(empty + 8 * i, kMaxWarps);
         }
-    } else {
-        const int T_ = p.P / p.top_k;
-        for (int i = threadIdx.x; i < T_ * nr; i += blockDim.x) {
-            const int t = i / nr, r = i - t * nr;
-            float acc = 0.f;
-            for (int j = 0; j < p.top_k; ++j) {
-                const int slot = t * p.top_k + j;
-                if (moe_expert(p.indices, slot, p.E, nullptr) < 0) continue;
-                float d = 0.f;
-                for (int s = 0; s < p.S; ++s) d += part[(int64_t)(slot * p.S + s) * p.rows_cta + r];
-                acc = __fmaf_rn(__ldg(p.weights + slot), d, acc);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    // The first kernel allows the second one only once everything before itself
+    // is complete; the second may therefore read indices and weights at once.
+    if (GLU) {
+        ptx::grid_dependency_wait();
+        ptx::grid_launch_dependents();
+    }
+    if (warp == 0) {
+        // ---------------- producer ----------------
+        int n = 0;
+        for (int rd = 0; rd < sp.rounds; ++rd) {
+            const int first = rd * sp.slots_round, count = min(sp.slots_round, p.P - first);
+            const int copies = count * NM * NA;
+            for (int st = 0; st < nst; ++st, ++n) {
+                const int slot_ = n % D;
+                const int rows = min(sp.rows_stage, nr - st * sp.rows_stage);
+                if (n >= D) ptx::mbar_wait(empty + 8 * slot_, ((n / D) - 1) & 1, p.err);
+                __syncwarp();
+                uint32_t bytes = 0;
+                for (int j = lane; j < count; j += 32)
+                    if (moe_expert(p.indices, first + j, p.E, nullptr) >= 0)
+                        bytes += (uint32_t)(NM * rows * (sp.row_bytes + (NA - 1) * sp.sb_bytes));
+                bytes = __reduce_add_sync(0xffffffffu, bytes);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(full + 8 * slot_, bytes);
+                __syncwarp();
+                for (int c = lane; c < copies; c += 32) {
+                    const int a = c % NA, m = c / NA % NM, j = c / (NA * NM);
+                    const int e = moe_expert(p.indices, first + j, p.E, nullptr);
+                    if (e < 0) continue;
+                    const int64_t row = (int64_t)e * p.R + r0 + (int64_t)st * sp.rows_stage;
+                    const uint8_t *src = a == 0 ? reinterpret_cast<const uint8_t *>(p.w[m].wq) + row * sp.row_bytes
+                                                : static_cast<const uint8_t *>(a == 1 ? p.w[m].scales : p.w[m].biases) +
+                                                      row * sp.sb_bytes;
+                    uint8_t *dst = ring + (size_t)slot_ * sp.stage_bytes + (j * NM + m) * mat_bytes +
+                                   (a == 0 ? 0 : sp.rows_stage * (sp.row_bytes + (a - 1) * sp.sb_bytes));
+                    ptx::bulk_g2s(ptx::smem_addr(dst), src, (uint32_t)(rows * (a == 0 ? sp.row_bytes : sp.sb_bytes)),
+                                  full + 8 * slot_);
+                }
             }
-            static_cast<T *>(p.out)[(int64_t)t * p.R + r0 + r] = Dt<T>::from_f(acc);
+        }
+        // No copy may land after the CTA has left.
+        if (lane == 0)
+            for (int k = max(0, n - D); k < n; ++k) ptx::mbar_drain(full + 8 * (k % D), (k / D) & 1, p.err);
+    } else {
+        // ---------------- consumers ----------------
+        if (!GLU) ptx::grid_dependency_wait();  // h
+        const int u = warp - 1, per_split = sp.slots_round * p.S;
+        const int split = u / per_split, j = u % per_split / p.S, seg = u % p.S;
+        const int64_t k0 = (int64_t)seg * kSeg + lane * 32;
+        const bool in = split < p.row_splits && k0 < p.C;
+        const int koff = in ? (int)(k0 / 2) : 0;
+        const int goff = in ? (int)(k0 >> p.gs_log) * (AFF ? 2 : 1) : 0;
+        int n = 0;
+        for (int rd = 0; rd < sp.rounds; ++rd) {
+            const int slot = rd * sp.slots_round + j;
+            const int e = split < p.row_splits && slot < p.P
+                              ? moe_expert(p.indices, slot, p.E, GLU && blockIdx.x == 0 && lane == 0 ? p.err : nullptr)
+                              : -1;
+            Slice sl;
+            if (e >= 0) {
+                float f[32];
+                const int64_t xr = GLU ? slot / p.top_k : slot;
+                load_slice<X>(static_cast<const X *>(p.x) + xr * p.C + k0, in, f);
+                make_slice<MODE>(f, sl);
+            }
+            for (int st = 0; st < nst; ++st, ++n) {
+                const int slot_ = n % D;
+                const int rows = min(sp.rows_stage, nr - st * sp.rows_stage);
+                const int per = (rows + p.row_splits - 1) / p.row_splits;
+                const int ra = min(rows, split * per), rb = min(rows, ra + per);
+                ptx::mbar_wait(full + 8 * slot_, (n / D) & 1, p.err);
+                if (e >= 0) {
+                    const uint8_t *base = ring + (size_t)slot_ * sp.stage_bytes + (size_t)(j * NM) * mat_bytes;
+                    for (int r = ra; r < rb; r += RB) {
+                        float v[kLoads];
+#pragma unroll
+                        for (int i = 0; i < kLoads; ++i) {
+                            const int row = min(r + i / NM, rb - 1), m = i % NM;
+                            const uint8_t *at = base + m * mat_bytes;
+                            const uint4 w = *reinterpret_cast<const uint4 *>(at + row * sp.row_bytes + koff);
+                            const uint8_t *sc = at + sp.rows_stage * sp.row_bytes + row * sp.sb_bytes + goff;
+                            uint32_t sb;
+                            if constexpr (AFF)
+                                sb = *reinterpret_cast<const uint16_t *>(sc) |
+                                     ((uint32_t)*reinterpret_cast<const uint16_t *>(sc + sp.rows_stage * sp.sb_bytes) << 16);
+                            else if constexpr (MODE == QMM_MODE_NVFP4)
+                                sb = *reinterpret_cast<const uint16_t *>(sc);
+                            else
+                                sb = *sc;
+                            v[i] = in ? dot_slice<T, MODE>(sl, w, sb) : 0.f;
+                        }
+                        const float t = reduce8(v, lane);
+                        if (lane < kLoads && r + lane / NM < rb)
+                            part[((int64_t)(slot * p.S + seg) * p.rows_cta + st * sp.rows_stage + r) * NM + lane] = t;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(empty + 8 * slot_);
+            }
         }
     }
+    __syncthreads();
+    finish_rows<T, GLU>(p, part, r0, nr);
+}
+
+// Shape of the streaming form for one product, or false where it does not
+// apply: contractions past 16 segments, or scale rows that a bulk copy cannot
+// take (not in whole 16-byte units).
+template <int MODE, bool GLU>
+bool plan_stream(StreamParams &sp, size_t &smem) {
+    constexpr int NM = GLU ? 2 : 1, NA = MODE == QMM_MODE_AFFINE ? 3 : 2, ES = MODE == QMM_MODE_AFFINE ? 2 : 1;
+    GemvParams &p = sp.g;
+    p.S = (int)((p.C + kSeg - 1) / kSeg);
+    const int64_t sb = (p.C >> p.gs_log) * ES;
+    if (p.S > kMaxWarps || sb % 16 != 0) return false;
+    sp.row_bytes = (int)(p.C / 2);
+    sp.sb_bytes = (int)sb;
+    sp.slots_round = std::min(p.P, kMaxWarps / p.S);
+    sp.rounds = (p.P + sp.slots_round - 1) / sp.slots_round;
+    p.row_splits = kMaxWarps / (sp.slots_round * p.S);
+    p.units = p.P * p.S;
+    // Partial sums of at most 32 KB; the ring takes what is left of 220 KB.
+    constexpr int64_t kPart = 32 * 1024, kRing = 220 * 1024 - kPart - 128;
+    int64_t rows = (p.R + num_sms() - 1) / num_sms();
+    rows = std::min<int64_t>(rows, kPart / ((int64_t)p.units * NM * 4));
+    if (rows < 1) return false;
+    p.rows_cta = (int)rows;
+    const int64_t row_all = (int64_t)sp.slots_round * NM * (sp.row_bytes + (NA - 1) * sp.sb_bytes);
+    int64_t rs = std::min<int64_t>(rows, (int64_t)(kLoads / NM) * p.row_splits);
+    rs = std::min(rs, rows <= kRing / row_all ? rows : kRing / 3 / row_all);
+    if (rs < 1) return false;
+    sp.rows_stage = (int)rs;
+    sp.stage_bytes = (int)(rs * row_all);
+    sp.stages = (int)std::min<int64_t>(8, kRing / sp.stage_bytes);
+    smem = 128 + (size_t)sp.stages * sp.stage_bytes + (size_t)p.units * rows * NM * 4;
+    return true;
 }
 
 template <typename T, typename X, int MODE, bool GLU>
 cudaError_t launch_half(GemvParams p, cudaStream_t s) {
     constexpr int NM = GLU ? 2 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    StreamParams sp{};
+    sp.g = p;
+    size_t ring = 0;
+    if (plan_stream<MODE, GLU>(sp, ring)) {
+        auto kern = moe_stream_kernel<T, X, MODE, GLU>;
+        struct StreamTag;
+        cudaError_t e = configure_once<StreamTag>((size_t)227 * 1024, [&]() {
+            return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        });
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3((unsigned)((p.R + sp.g.rows_cta - 1) / sp.g.rows_cta), 1, 1);
+        cfg.blockDim = dim3(32 * (kMaxWarps + 1), 1, 1);
+        cfg.dynamicSmemBytes = ring;
+        e = cudaLaunchKernelEx(&cfg, kern, sp);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+        return cudaGetLastError();
+    }
     p.S = (int)((p.C + kSeg - 1) / kSeg);
     p.units = p.P * p.S;
     p.unit_warps = std::min(p.units, kMaxWarps);
@@ -355,16 +565,9 @@ cudaError_t launch_half(GemvParams p, cudaStream_t s) {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.R + rows - 1) / rows), 1, 1);
     cfg.blockDim = dim3(32 * p.unit_warps * p.row_splits, 1, 1);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess) return e;
     count_launches(1);

@@ -67,13 +67,35 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
     return v;
 }
 
+// Value of an E8M0 byte without branches: 2^(s - 127), for s = 0 the subnormal
+// 2^-127, for s = 255 NaN (the infinity's bits with one mantissa bit set).
+__device__ __forceinline__ float e8m0(uint32_t s) {
+    return __uint_as_float(max((s << 23) | (((s + 1u) << 14) & 0x00400000u), 0x00400000u));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
 // Eight E2M1 codes as unsigned bytes 128 + 2 e, four per word: a byte
 // permutation of the table of doubled magnitudes by the raw nibbles gives the
 // magnitude of every non-negative code and 0 for a negative one (selector bit
 // 3 asks for the sign of a table byte), by the nibbles with their sign bits
 // flipped the converse; 128 + pos - neg cannot borrow between bytes.
-__device__ __forceinline__ void e2m1_bytes(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    constexpr uint32_t A = 0x03020100u, B = 0x0C080604u;
+// A, B: the table, held in registers by the caller (as constants they were
+// set up again before every permutation).
+__device__ __forceinline__ void e2m1_bytes(uint32_t A, uint32_t B, uint32_t w, uint32_t &lo, uint32_t &hi) {
     const uint32_t n = w ^ 0x88888888u;
     lo = prmt(A, B, w) + 0x80808080u - prmt(A, B, n);
     hi = prmt(A, B, w >> 16) + 0x80808080u - prmt(A, B, n >> 16);
@@ -84,9 +106,10 @@ __device__ __forceinline__ void e2m1_bytes(uint32_t w, uint32_t &lo, uint32_t &h
 // the offset of the codes (E2M1; two groups for nvfp4) needs.
 struct Slice {
     int x[16];
-    float unit;      // 2^-sh; NaN if any activation is infinite or NaN
+    float unit;      // 2^-sh (E2M1: half of it, the codes being doubled); NaN if any activation is infinite or NaN
     float xsum;      // affine: sum of the activations
     int off[2];      // E2M1: -128 * sum of the integers of each half
+    uint32_t ta, tb; // E2M1: doubled magnitudes of codes 0..7, a byte each
 };
 
 // Element of half h (0, 1) of pair k within a word of eight codes.  Affine
@@ -125,6 +148,8 @@ __device__ __forceinline__ void load_slice(const X *x, bool ok, float (&f)[32]) 
 
 template <int MODE>
 __device__ __forceinline__ void make_slice(const float (&f)[32], Slice &s) {
+    asm volatile("mov.u32 %0, 0x03020100;" : "=r"(s.ta));
+    asm volatile("mov.u32 %0, 0x0C080604;" : "=r"(s.tb));
     uint32_t mb = 0;  // largest |x| by bit pattern (infinities and NaN largest)
 #pragma unroll
     for (int i = 0; i < 32; ++i) mb = max(mb, __float_as_uint(f[i]) & 0x7FFFFFFFu);
@@ -150,6 +175,7 @@ __device__ __forceinline__ void make_slice(const float (&f)[32], Slice &s) {
     }
     const int s0 = (int)(sum[0] - 16u * 0x4B400000u), s1 = (int)(sum[1] - 16u * 0x4B400000u);
     s.xsum = s.unit * (float)(s0 + s1);
+    if constexpr (MODE != QMM_MODE_AFFINE) s.unit *= 0.5f;
     if constexpr (MODE == QMM_MODE_NVFP4) {
         s.off[0] = -128 * s0;
         s.off[1] = -128 * s1;
@@ -186,7 +212,7 @@ __device__ __forceinline__ float dot_slice(const Slice &s, const uint4 &w, uint3
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t lo, hi;
-            e2m1_bytes(ws[i], lo, hi);
+            e2m1_bytes(s.ta, s.tb, ws[i], lo, hi);
             int &c0 = (NV && i >= 2) ? b0 : a0;
             int &c1 = (NV && i >= 2) ? b1 : a1;
             c0 = dp2a_lo(s.x[4 * i], lo, c0);
@@ -194,13 +220,13 @@ __device__ __forceinline__ float dot_slice(const Slice &s, const uint4 &w, uint3
             c0 = dp2a_lo(s.x[4 * i + 2], hi, c0);
             c1 = dp2a_hi(s.x[4 * i + 3], hi, c1);
         }
-        const float x0 = 0.5f * mxf::scale_value<MODE>(sb & 0xFFu);
-        float c = (x0 * s.unit) * (float)(a0 + a1);
         if constexpr (NV) {
-            const float x1 = 0.5f * mxf::scale_value<MODE>((sb >> 8) & 0xFFu);
-            c = __fmaf_rn(x1 * s.unit, (float)(b0 + b1), c);
+            const uint32_t h = mxf::e4m3x2_to_h2(sb, 0);
+            const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            return __fmaf_rn(x.y * s.unit, (float)(b0 + b1), (x.x * s.unit) * (float)(a0 + a1));
+        } else {
+            return (e8m0(sb) * s.unit) * (float)(a0 + a1);
         }
-        return c;
     }
 }
 
@@ -325,7 +351,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) moe_gemv_kernel(const GemvP
         auto use = [&](int r, const uint4 (&w)[kLoads], const uint32_t (&s)[kLoads]) {
             float v[kLoads];
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) v[i] = ok ? dot_slice<T, MODE>(sl, w[i], s[i]) : 0.f;
+            for (int i = 0; i < kLoads; ++i) v[i] = dot_slice<T, MODE>(sl, w[i], s[i]);  // (0 where !ok)
             const float t = reduce8(v, lane);
             if (lane < kLoads && r + lane / NM < rb)
                 part[((int64_t)u * p.rows_cta + r) * NM + lane] = t;
@@ -456,28 +482,35 @@ __global__ void __launch_bounds__(32 * (kMaxWarps + 1), 1) moe_stream_kernel(con
                 const int ra = min(rows, split * per), rb = min(rows, ra + per);
                 ptx::mbar_wait(full + 8 * slot_, (n / D) & 1, p.err);
                 if (e >= 0) {
-                    const uint8_t *base = ring + (size_t)slot_ * sp.stage_bytes + (size_t)(j * NM) * mat_bytes;
+                    const uint32_t at0 = ptx::smem_addr(ring) + slot_ * sp.stage_bytes + j * NM * mat_bytes;
+                    float *out = part + ((slot * p.S + seg) * p.rows_cta + st * sp.rows_stage) * NM;
                     for (int r = ra; r < rb; r += RB) {
+                        // (a batch past the split's end repeats its last row, whose sums are dropped)
+                        uint32_t cw = at0 + r * sp.row_bytes + koff;
+                        uint32_t cs = at0 + sp.rows_stage * sp.row_bytes + r * sp.sb_bytes + goff;
                         float v[kLoads];
 #pragma unroll
-                        for (int i = 0; i < kLoads; ++i) {
-                            const int row = min(r + i / NM, rb - 1), m = i % NM;
-                            const uint8_t *at = base + m * mat_bytes;
-                            const uint4 w = *reinterpret_cast<const uint4 *>(at + row * sp.row_bytes + koff);
-                            const uint8_t *sc = at + sp.rows_stage * sp.row_bytes + row * sp.sb_bytes + goff;
-                            uint32_t sb;
-                            if constexpr (AFF)
-                                sb = *reinterpret_cast<const uint16_t *>(sc) |
-                                     ((uint32_t)*reinterpret_cast<const uint16_t *>(sc + sp.rows_stage * sp.sb_bytes) << 16);
-                            else if constexpr (MODE == QMM_MODE_NVFP4)
-                                sb = *reinterpret_cast<const uint16_t *>(sc);
-                            else
-                                sb = *sc;
-                            v[i] = in ? dot_slice<T, MODE>(sl, w, sb) : 0.f;
+                        for (int i = 0; i < RB; ++i) {
+#pragma unroll
+                            for (int m = 0; m < NM; ++m) {
+                                const uint4 w = lds128(cw + m * mat_bytes);
+                                uint32_t sb;
+                                if constexpr (AFF)
+                                    sb = lds16(cs + m * mat_bytes) |
+                                         (lds16(cs + m * mat_bytes + sp.rows_stage * sp.sb_bytes) << 16);
+                                else if constexpr (MODE == QMM_MODE_NVFP4)
+                                    sb = lds16(cs + m * mat_bytes);
+                                else
+                                    sb = lds8(cs + m * mat_bytes);
+                                v[i * NM + m] = dot_slice<T, MODE>(sl, w, sb);
+                            }
+                            if (r + i + 1 < rb) {
+                                cw += sp.row_bytes;
+                                cs += sp.sb_bytes;
+                            }
                         }
                         const float t = reduce8(v, lane);
-                        if (lane < kLoads && r + lane / NM < rb)
-                            part[((int64_t)(slot * p.S + seg) * p.rows_cta + st * sp.rows_stage + r) * NM + lane] = t;
+                        if (lane < kLoads && r + lane / NM < rb) out[r * NM + lane] = t;
                     }
                 }
                 __syncwarp();

@@ -29,22 +29,31 @@
 // X * element exactly.  Scales for which that factor leaves the type's range
 // take the element values in fp32 instead.
 //
-// Roles (one CTA per SM, 25 warps, persistent over chunk x 128-row tiles):
-//   0-15   dequantize, four groups of four warps; group g takes block g of each
-//          four, thread r of a group owns weight row r;
-//   16-19  epilogue;  20 MMA issuer, owner of tensor memory;
-//   21, 22 TMA of packed tiles (gate and up, or the down tile), 256 k at a time;
-//   23     TMA of activation tiles;
-//   24     scale (and bias) windows of 16 bytes a row, by asynchronous copies.
+// Roles (one CTA per SM, 25 warps, persistent over chunk x 128-row tiles; the
+// roles that everything waits for have the lowest warp numbers):
+//   0-3    epilogue;
+//   4      issues the MMAs, by one lane;
+//   5, 6   TMA of packed tiles (gate and up, or the down tile), 256 k at a time,
+//          and of their scales (and biases), a window of 16 bytes a row;
+//   7      TMA of activation tiles;
+//   8-23   dequantize, four groups of four warps; group g takes block g of each
+//          packed tile;
+//   24     scale windows by asynchronous copies, where a row of scales is not
+//          made of whole 16 bytes.
 // Three rings: packed tiles and windows, activation tiles, and dequantized
-// blocks in tensor memory.  TMA issues cost their thread several hundred cycles
-// each whatever their size, so a packed tile is 256 elements wide and an
+// blocks in tensor memory.  A barrier's hand-over costs its waiter 150 cycles
+// and more even when it need not wait, an MMA 40 and a TMA 200 cycles of their
+// thread, whatever their sizes: so a packed tile is 256 elements wide, an
 // activation tile comes in one box as high as the chunk needs (heights in
-// kHeights).
+// kHeights), and k-blocks reach the MMA thread in units of 4 (of 2 with tall
+// chunks, whose accumulators leave less tensor memory).
 //
-// Bound: with few rows per expert the dequantize warps' integer instructions
-// (about 3 per element), above HBM's time by half; with many rows the tensor
-// cores.
+// Bound: with few rows per expert the dequantize warps' instructions (about 3
+// per element), with many rows the tensor cores and, on short contractions, the
+// epilogue.  2048 rows, 8 experts 4096 x 14336, 2 each, nvfp4: gate/up 706 us,
+// down 417 us (1.29e15 operations a second); 512 rows: 241 and 170 us.  Two CTAs
+// sharing an activation tile (MMAs of 256 rows) measured 741 and 446, 292 and
+// 200 us: the hand-overs between the two cost more than the halved copies save.
 #include <cuda.h>
 
 #include <algorithm>
@@ -59,25 +68,35 @@ namespace {
 
 constexpr int kGroups = 4;
 constexpr int kDqWarps = 4 * kGroups;
-constexpr int kEpiWarp = kDqWarps;        // 16..19
-constexpr int kMmaWarp = kEpiWarp + 4;    // 20
-constexpr int kWWarp = kMmaWarp + 1;      // 21, 22
-constexpr int kBWarp = kWWarp + 2;        // 23
-constexpr int kSWarp = kBWarp + 1;        // 24
+constexpr int kMmaWarp = 4;               // after the epilogue's 0..3
+constexpr int kWWarp = kMmaWarp + 1;      // 5, 6
+constexpr int kBWarp = kWWarp + 2;        // 7
+constexpr int kDqWarp = kBWarp + 1;       // 8..23: a multiple of 4, warp % 4 is the tensor memory quarter
+constexpr int kSWarp = kDqWarp + kDqWarps;  // 24
 constexpr int kThreads = 32 * (kSWarp + 1);
 constexpr int kBM = 128, kBK = 64;
 constexpr int kStageK = kBK * kGroups;    // k per packed stage
 constexpr int kPBytes = kBM * kStageK / 2;  // 16 KB
 constexpr int kWinBytes = kBM * 16;       // one window of 16 bytes per row
-constexpr int kPair = 2;                  // k-blocks per hand-over to the MMA
-constexpr int kRing = 8;                  // hand-over barriers (more than pairs in flight)
+constexpr int kRing = 8;                  // hand-over barriers (more than units in flight)
 constexpr int kBarBytes = 1024;           // barriers and the tensor-memory address
+constexpr int kMaxCap = 192;              // activation rows of a tile at most
 constexpr int kNumHeights = 6;
 constexpr int kHeights[kNumHeights] = {16, 32, 64, 96, 128, 192};
 
+// Chunks of at most CAP rows: two accumulators of CAP columns leave room for NU
+// units of U dequantized k-blocks (32 columns each) in tensor memory; SB units
+// of activations lie in shared memory.
+template <int CAP>
+struct TileCfg {
+    static constexpr int U = CAP <= 64 ? 4 : 2;
+    static constexpr int NU = (512 - 2 * CAP) / (32 * U);
+    static constexpr int SB = 3;
+    static constexpr int BBytes = CAP * 128 * U;
+};
+
 struct MoeHeader {
     int num_chunks;
-    int valid;  // slots with an expert (sorted first)
 };
 
 struct MoePlan {
@@ -89,15 +108,20 @@ struct ActMaps {
     CUtensorMap m[kNumHeights];
 };
 
+// Per weight matrix: packed codes, and where whole 16-byte windows allow it
+// scales and biases.
+struct WeightMaps {
+    CUtensorMap w[2], s[2], b[2];
+};
+
 struct TcParams {
     const void *scales[2], *biases[2];
     void *out;                // h [R / 64][rows][64] T, or parts [slots][R] fp32
     int64_t row_bytes_sb;     // bytes of one row of scales
     int rows;                 // slots
     int R, KB, gs_log, n_tiles;
-    int acc_stride, na;       // columns per accumulator; pairs of A slots
-    int SP, SB, b_bytes;      // ring depths; bytes of an activation stage (a pair of k-blocks)
-    int sb_vec;               // scale copies of 16, 4 or 2 bytes
+    int SP;                   // packed stages
+    int sb_vec;               // scale windows by TMA (16), or by copies of 4 or 2 bytes
     int act;
     const MoeHeader *hdr;
     const int4 *chunks;       // {expert, first sorted row, rows, box (box_of)}
@@ -251,9 +275,6 @@ __device__ __forceinline__ float gate_fast(float g, int act) {
     return __fdividef(g, 1.f + __expf(-z));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -268,6 +289,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 // looked at only once a wait has gone on for long.  On timeout the device error
 // word is set and the caller carries on in bounds.
 __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, int *err) {
+    if (ptx::mbar_test(bar, parity)) return;
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
         if (ptx::mbar_try_wait(bar, parity)) return;
@@ -287,9 +309,9 @@ struct Ring {
     }
 };
 
-template <typename T, int MODE, bool GLU>
+template <typename T, int MODE, bool GLU, int CAP>
 __global__ void __launch_bounds__(kThreads, 1)
-moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
+moe_tc_kernel(const __grid_constant__ WeightMaps maps,
               const __grid_constant__ ActMaps map_b, const __grid_constant__ TcParams p) {
     constexpr bool AFF = MODE == QMM_MODE_AFFINE;
     constexpr int NW = AFF ? 2 : 1;             // windows per stage: scales (and biases)
@@ -300,14 +322,16 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
-    const int SP = p.SP, SB = p.SB;
-    const uint32_t NA = p.na;
+    using Cfg = TileCfg<CAP>;
+    constexpr int U = Cfg::U, SB = Cfg::SB, BB = Cfg::BBytes;
+    constexpr uint32_t NU = Cfg::NU;
+    const int SP = p.SP;
     // Barriers first, then the rings: activations, packed tiles, windows.
-    const uint32_t bars = base, b0 = base + kBarBytes, p0 = b0 + SB * p.b_bytes, s0 = p0 + SP * kPBytes;
-    // full_p, empty_p: packed stages.  Pair n of k-blocks (counted over all of
-    // the CTA's tiles) is handed over on ready[n % kRing]: eight dequantize
-    // warps and the activation tile's bytes; its MMAs complete done[n % kRing],
-    // which frees pair slot n % NA of A and activation stage n % SB.
+    const uint32_t bars = base, b0 = base + kBarBytes, p0 = b0 + SB * BB, s0 = p0 + SP * kPBytes;
+    // full_p, empty_p: packed stages.  Unit n of k-blocks (counted over all of
+    // the CTA's tiles) is handed over on ready[n % kRing]: four dequantize warps
+    // per k-block and the activation tile's bytes; its MMAs complete
+    // done[n % kRing], which frees slot n % NU of A and activation stage n % SB.
     const uint32_t full_p = bars, empty_p = full_p + 8 * SP, ready = empty_p + 8 * SP, done = ready + 8 * kRing;
     const uint32_t acc_full = done + 8 * kRing, acc_empty = acc_full + 16, fin = acc_empty + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + (fin + 8 - base));
@@ -315,11 +339,11 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < SP; ++i) {
-            ptx::mbar_init(full_p + 8 * i, NM + 32);
+            ptx::mbar_init(full_p + 8 * i, NM + (p.sb_vec == 16 ? 0 : 32));
             ptx::mbar_init(empty_p + 8 * i, kDqWarps);
         }
         for (int i = 0; i < kRing; ++i) {
-            ptx::mbar_init(ready + 8 * i, 4 * kPair + 1);
+            ptx::mbar_init(ready + 8 * i, 4 * U + 1);
             ptx::mbar_init(done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -340,13 +364,13 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
     // What the preceding kernels wrote (chunks, activations) is read from here on.
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int KB = p.KB, KS = (KB + kGroups - 1) / kGroups, KP = (KB + kPair - 1) / kPair;
+    const int KB = p.KB, KS = (KB + kGroups - 1) / kGroups, KU = (KB + U - 1) / U;
     const int num_tiles = p.hdr->num_chunks * p.n_tiles;
-    const uint32_t a_col0 = 2u * p.acc_stride;
+    const uint32_t a_col0 = 2u * CAP;
 
-    if (warp < kDqWarps) {
+    if (warp >= kDqWarp && warp < kSWarp) {
         // ------------------------- dequantize -------------------------
-        const int g = warp >> 2, q = warp & 3;
+        const int g = (warp - kDqWarp) >> 2, q = warp & 3;
         const int row = GLU ? 16 * q + (lane & 15) + ((lane & 16) << 2) : 32 * q + lane;
         const uint8_t *prow = gbase + (p0 - base) + row * (kStageK / 2);
         const uint8_t *swin = gbase + (s0 - base) + row * 16;
@@ -386,10 +410,10 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                     dequant_block<T, MODE>(w, sb, bb, v);
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
-                    const uint32_t n = c + kb / kPair;
-                    if (n >= NA) wait_phase(done + 8 * ((n - NA) % kRing), ((n - NA) / kRing) & 1, p.err);
+                    const uint32_t n = c + kb / U;
+                    if (n >= NU) wait_phase(done + 8 * ((n - NU) % kRing), ((n - NU) / kRing) & 1, p.err);
                     tc_fence_after();
-                    tmem_st32(dst + 64u * (n & (NA - 1)) + 32u * (kb & 1), v);
+                    tmem_st32(dst + 32u * U * (n % NU) + 32u * (kb % U), v);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -397,15 +421,15 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                 } else {
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
-                    if (kb == KB && (kb & 1)) {  // the missing half of the tile's last pair
-                        const uint32_t n = c + kb / kPair;
-                        if (n >= NA) wait_phase(done + 8 * ((n - NA) % kRing), ((n - NA) / kRing) & 1, p.err);
+                    if (kb / U < KU) {  // missing from the tile's last unit
+                        const uint32_t n = c + kb / U;
+                        if (n >= NU) wait_phase(done + 8 * ((n - NU) % kRing), ((n - NU) / kRing) & 1, p.err);
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(ready + 8 * (n % kRing));
                     }
                 }
             }
-            c += KP;
+            c += KU;
         }
     } else if (warp < kMmaWarp) {
         // ------------------------- epilogue -------------------------
@@ -420,7 +444,7 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
             const int nj = (ch.z + 31) / 32;
             for (int j = 0; j < nj; ++j) {
                 uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + acc * p.acc_stride + 32 * j, v);
+                tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + acc * CAP + 32 * j, v);
                 tmem_ld_wait();
                 if (j == nj - 1) {
                     tc_fence_before();
@@ -472,23 +496,23 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                 const uint32_t zstep = (uint32_t)(ch.w >> 8) * 128u >> 4;  // descriptor step of one k-block
                 if (i >= 2) wait_phase(acc_empty + 8 * acc, (use + 1) & 1, p.err);
                 tc_fence_after();
-                const uint32_t d = tmem + acc * p.acc_stride;
-                for (int kp = 0; kp < KP; ++kp, ++n) {
+                const uint32_t d = tmem + acc * CAP;
+                for (int ku = 0; ku < KU; ++ku, ++n) {
                     wait_phase(ready + 8 * (n % kRing), (n / kRing) & 1, p.err);
                     tc_fence_after();
-                    uint64_t db = sw128_desc(b0 + bslot * p.b_bytes);
-                    uint32_t ta = tmem + a_col0 + 64u * (n & (NA - 1));
-                    tc_mma_ts(d, ta, db, idesc, kp != 0);
-                    tc_mma_ts(d, ta + 8, db + 2, idesc, 1);
-                    tc_mma_ts(d, ta + 16, db + 4, idesc, 1);
-                    tc_mma_ts(d, ta + 24, db + 6, idesc, 1);
-                    if (2 * kp + 1 < KB) {
-                        db += zstep;
+                    uint64_t db = sw128_desc(b0 + bslot * BB);
+                    uint32_t ta = tmem + a_col0 + 32u * U * (n % NU);
+                    const int blocks = min(U, KB - U * ku);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (u < blocks) {
+                            tc_mma_ts(d, ta, db, idesc, ku != 0 || u != 0);
+                            tc_mma_ts(d, ta + 8, db + 2, idesc, 1);
+                            tc_mma_ts(d, ta + 16, db + 4, idesc, 1);
+                            tc_mma_ts(d, ta + 24, db + 6, idesc, 1);
+                        }
                         ta += 32;
-                        tc_mma_ts(d, ta, db, idesc, 1);
-                        tc_mma_ts(d, ta + 8, db + 2, idesc, 1);
-                        tc_mma_ts(d, ta + 16, db + 4, idesc, 1);
-                        tc_mma_ts(d, ta + 24, db + 6, idesc, 1);
+                        db += zstep;
                     }
                     tc_commit(done + 8 * (n % kRing));
                     if (++bslot == SB) bslot = 0;
@@ -504,8 +528,11 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
         // ------------------------- packed tiles -------------------------
         const int m = warp - kWWarp;
         if (lane == 0 && m < NM) {
-            const CUtensorMap *map = m == 0 ? &map_w0 : &map_w1;
-            constexpr uint32_t bytes = kPBytes / NM;
+            const CUtensorMap *map = &maps.w[m];
+            constexpr uint32_t bytes = kPBytes / NM, sbytes = kWinBytes / NM;
+            constexpr int ES = AFF ? 2 : 1;
+            const bool windows = p.sb_vec == 16;
+            const uint32_t total = bytes + (windows ? NW * sbytes : 0u);
             Ring ps;
             int n = 0;
             for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
@@ -513,9 +540,15 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
                 const int r0 = ch.x * p.R + (tile % p.n_tiles) * (kBM / NM);
                 for (int st = 0; st < KS; ++st, ++n, ps.next(SP)) {
                     if (ps.wrapped) wait_phase(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
-                    ptx::mbar_arrive_expect_tx(full_p + 8 * ps.slot, bytes);
+                    ptx::mbar_arrive_expect_tx(full_p + 8 * ps.slot, total);
                     tma_load_2d(p0 + ps.slot * kPBytes + m * bytes, map, st * (kStageK / 8), r0,
                                 full_p + 8 * ps.slot);
+                    if (windows) {
+                        const int at = (((st * kStageK) >> p.gs_log) * ES & ~15) / ES;
+                        const uint32_t win = s0 + ps.slot * (NW * kWinBytes) + m * sbytes;
+                        tma_load_2d(win, &maps.s[m], at, r0, full_p + 8 * ps.slot);
+                        if constexpr (AFF) tma_load_2d(win + kWinBytes, &maps.b[m], at, r0, full_p + 8 * ps.slot);
+                    }
                 }
             }
             for (int k = max(0, n - SP); k < n; ++k) ptx::mbar_drain(full_p + 8 * (k % SP), (k / SP) & 1, p.err);
@@ -530,18 +563,18 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
             for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
                 const int4 ch = p.chunks[tile / p.n_tiles];
                 const CUtensorMap *map = &map_b.m[ch.w & 255];
-                const uint32_t bytes = (uint32_t)(ch.w >> 8) * 128u * kPair;
-                for (int kp = 0; kp < KP; ++kp, ++n) {
+                const uint32_t bytes = (uint32_t)(ch.w >> 8) * 128u * U;
+                for (int ku = 0; ku < KU; ++ku, ++n) {
                     if (n >= (uint32_t)SB) wait_phase(done + 8 * ((n - SB) % kRing), ((n - SB) / kRing) & 1, p.err);
                     ptx::mbar_arrive_expect_tx(ready + 8 * (n % kRing), bytes);
-                    tma_load_3d(b0 + slot * p.b_bytes, map, 0, ch.y, kPair * kp, ready + 8 * (n % kRing));
+                    tma_load_3d(b0 + slot * BB, map, 0, ch.y, U * ku, ready + 8 * (n % kRing));
                     if (++slot == SB) slot = 0;
                 }
             }
             for (uint32_t k = n < (uint32_t)SB ? 0 : n - SB; k < n; ++k)
                 ptx::mbar_drain(ready + 8 * (k % kRing), (k / kRing) & 1, p.err);
         }
-    } else {
+    } else if (p.sb_vec != 16) {
         // ------------------------- scale windows -------------------------
         constexpr int ES = AFF ? 2 : 1;
         Ring ps;
@@ -571,9 +604,7 @@ moe_tc_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant_
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
                         const uint32_t d = win + w * kWinBytes + i * 512;
-                        if (p.sb_vec == 16) {
-                            cp_async16(d, src[i][w] + at);
-                        } else if (p.sb_vec == 4) {
+                        if (p.sb_vec == 4) {
                             for (int o = 0; o < left; o += 4) cp_async4(d + o, src[i][w] + at + o);
                         } else {
                             for (int o = 0; o < left; o += 2)
@@ -757,10 +788,7 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const PrepParams
             p.chunks[nch[k] + j] = make_int4(k, first[k] + j * size, n, box_of(n));
         }
     }
-    if (tid == 0) {
-        p.hdr->num_chunks = nch[E];
-        p.hdr->valid = first[E];
-    }
+    if (tid == 0) p.hdr->num_chunks = nch[E];
 }
 
 // y[t] = sum over slots in order of weight * part, rounded once.
@@ -846,28 +874,40 @@ cudaError_t launch_chained(dim3 grid, int threads, size_t smem, cudaStream_t s, 
 
 // Rows per chunk at most: an expert's rows mostly fit one narrow chunk when
 // there are few of them, and the rings hold more packed stages then.
-int chunk_cap(int64_t slots, int64_t E) { return slots <= 32 * E ? 64 : 192; }
+int chunk_cap(int64_t slots, int64_t E) { return slots <= 32 * E ? 64 : kMaxCap; }
 
-template <typename T, int MODE, bool GLU>
-cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStream_t s) {
+template <typename T, int MODE, bool GLU, int CAP>
+cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) {
+    using Cfg = TileCfg<CAP>;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     const int64_t P = a.T * a.top_k, C = GLU ? a.K : a.I, R = GLU ? a.I : a.N;
     constexpr int NM = GLU ? 2 : 1, NW = MODE == QMM_MODE_AFFINE ? 2 : 1;
     constexpr int ES = MODE == QMM_MODE_AFFINE ? 2 : 1;
     const ExpertWeight *ew[2] = {GLU ? &a.gate : &a.down, GLU ? &a.up : &a.down};
-    CUtensorMap mw[2];
-    for (int m = 0; m < 2; ++m)
-        if (!make_map_2d(&mw[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, ew[m]->wq, (uint64_t)C / 8,
-                         (uint64_t)(a.n_experts * R), (uint64_t)C / 2, kStageK / 8, kBM / NM,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
-            return cudaErrorInvalidValue;
     TcParams p{};
+    p.row_bytes_sb = C / a.group_size * ES;
+    p.sb_vec = p.row_bytes_sb % 16 == 0 ? 16 : (p.row_bytes_sb % 4 == 0 ? 4 : 2);
+    WeightMaps mw{};
+    const uint64_t rows = (uint64_t)(a.n_experts * R);
+    const CUtensorMapDataType st = ES == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    for (int m = 0; m < NM; ++m) {
+        auto window = [&](CUtensorMap *map, const void *ptr) {
+            return make_map_2d(map, st, ptr, (uint64_t)(C / a.group_size), rows, (uint64_t)p.row_bytes_sb, 16 / ES,
+                               kBM / NM, CU_TENSOR_MAP_SWIZZLE_NONE);
+        };
+        if (!make_map_2d(&mw.w[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, ew[m]->wq, (uint64_t)C / 8, rows, (uint64_t)C / 2,
+                         kStageK / 8, kBM / NM, CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+        if (p.sb_vec == 16 &&
+            (!window(&mw.s[m], ew[m]->scales) || (NW == 2 && !window(&mw.b[m], ew[m]->biases))))
+            return cudaErrorInvalidValue;
+    }
     ActMaps mb;
     const uint64_t dims[3] = {64, (uint64_t)P, (uint64_t)C / 64};
     // x rows as they are ([slots][K], k-blocks 128 bytes apart); h by k-blocks
     const uint64_t strides[2] = {GLU ? (uint64_t)C * 2 : 128, GLU ? 128 : (uint64_t)P * 128};
     for (int i = 0; i < kNumHeights; ++i) {
-        const uint32_t box[3] = {64, (uint32_t)kHeights[i], kPair};
+        const uint32_t box[3] = {64, (uint32_t)kHeights[i], (uint32_t)Cfg::U};
         if (!make_map(&mb.m[i], std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                       3, ws + (GLU ? w.x : w.h), dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -878,29 +918,23 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStr
         p.biases[m] = ew[m]->biases;
     }
     p.out = ws + (GLU ? w.h : w.parts);
-    p.row_bytes_sb = C / a.group_size * ES;
-    p.sb_vec = p.row_bytes_sb % 16 == 0 ? 16 : (p.row_bytes_sb % 4 == 0 ? 4 : 2);
     p.rows = (int)P;
     p.R = (int)R;
     p.KB = (int)(C / kBK);
     p.gs_log = a.group_size == 16 ? 4 : (a.group_size == 32 ? 5 : (a.group_size == 64 ? 6 : 7));
     p.n_tiles = (int)((R + kBM / NM - 1) / (kBM / NM));
-    p.acc_stride = cap <= 128 ? 128 : 192;
-    p.na = cap <= 128 ? 4 : 2;
-    p.b_bytes = cap * 128 * kPair;
-    p.SB = cap <= 64 ? 5 : 3;
     constexpr size_t kSmemMax = 227 * 1024;
     const size_t fixed = 1024 + kBarBytes;  // alignment; barriers
     const size_t p_bytes = kPBytes + NW * kWinBytes;
-    p.SP = (int)std::min<size_t>(8, (kSmemMax - fixed - (size_t)p.SB * p.b_bytes) / p_bytes);
+    p.SP = (int)std::min<size_t>(8, (kSmemMax - fixed - (size_t)Cfg::SB * Cfg::BBytes) / p_bytes);
     if (p.SP < 2) return cudaErrorInvalidConfiguration;
-    const size_t smem = fixed + (size_t)p.SB * p.b_bytes + p.SP * p_bytes;
+    const size_t smem = fixed + (size_t)Cfg::SB * Cfg::BBytes + p.SP * p_bytes;
     p.act = a.act;
     p.hdr = reinterpret_cast<const MoeHeader *>(ws + w.hdr);
     p.chunks = reinterpret_cast<const int4 *>(ws + w.chunks);
     p.perm = reinterpret_cast<const int32_t *>(ws + w.perm);
     p.err = device_error_word();
-    auto kern = moe_tc_kernel<T, MODE, GLU>;
+    auto kern = moe_tc_kernel<T, MODE, GLU, CAP>;
     struct Tag;
     cudaError_t e = configure_once<Tag>(kSmemMax, [&]() {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
@@ -908,7 +942,7 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, int cap, cudaStr
     if (e != cudaSuccess) return e;
     const int64_t most = std::min<int64_t>(w.max_chunks, std::min<int64_t>(P, a.n_experts) + P / 16) * p.n_tiles;
     const int grid = (int)std::min<int64_t>(std::max<int64_t>(most, 1), num_sms());
-    return launch_chained<moe_tc_kernel<T, MODE, GLU>>(dim3(grid), kThreads, smem, s, mw[0], mw[1], mb, p);
+    return launch_chained<moe_tc_kernel<T, MODE, GLU, CAP>>(dim3(grid), kThreads, smem, s, mw, mb, p);
 }
 
 template <typename T, int MODE>
@@ -939,8 +973,13 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
     const size_t smem = (size_t)(3 * (pp.E + 2)) * sizeof(int);
     cudaError_t e = launch_chained<moe_prep_kernel>(dim3((unsigned)((P + pp.seg - 1) / pp.seg)), kPrepThreads, smem, s, pp);
     if (e != cudaSuccess) return e;
-    if ((e = run_product<T, MODE, true>(a, w, cap, s)) != cudaSuccess) return e;
-    if ((e = run_product<T, MODE, false>(a, w, cap, s)) != cudaSuccess) return e;
+    if (cap <= 64) {
+        if ((e = run_product<T, MODE, true, 64>(a, w, s)) != cudaSuccess) return e;
+        if ((e = run_product<T, MODE, false, 64>(a, w, s)) != cudaSuccess) return e;
+    } else {
+        if ((e = run_product<T, MODE, true, kMaxCap>(a, w, s)) != cudaSuccess) return e;
+        if ((e = run_product<T, MODE, false, kMaxCap>(a, w, s)) != cudaSuccess) return e;
+    }
 
     const float *parts = reinterpret_cast<const float *>(ws + w.parts);
     const bool vec4 = a.N % 4 == 0;

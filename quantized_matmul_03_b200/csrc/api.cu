@@ -126,8 +126,20 @@ bool gather_tc_supported(qmm_dtype dtype, int64_t x_batch, int64_t M, int64_t K,
     return gemm_grouped_supported(dtype, probe) && gather_prep_fits(n_experts);
 }
 
-// Slots up to which qmm_moe_experts takes the few-row kernels.
-constexpr int64_t kMoeGemvSlots = 16;
+// Whether qmm_moe_experts takes the few-row kernels.  They expand every slot's
+// expert, the tensor-core path every touched expert once, at nearly the same
+// rate (about 5.5e12 weights a second), and the latter costs about 25 us more
+// per call (sort, combine, tiles that are mostly empty): few rows while the
+// slots beyond the number of experts they are expected to touch cost less than
+// that.  Measured, few-row / tensor-core path: 4 and 6 slots over 8 experts
+// 4096 x 14336 127 / 148 and 193 / 178 us; 16 and 32 slots over 16 experts 2048
+// x 2048 53 / 57 and 94 / 74; 64 and 96 slots over 64 experts 2048 x 1024 88 /
+// 90 and 131 / 102.
+bool moe_few_rows(const ExpertsArgs &a) {
+    const double slots = (double)a.T * a.top_k, E = (double)a.n_experts;
+    const double touched = E * (1.0 - std::pow(1.0 - 1.0 / E, slots));
+    return slots <= 64 && (slots - touched) * (double)a.I * (2.0 * a.K + a.N) <= 1.4e8;
+}
 
 qmm_status finish_launch(cudaError_t e, const char *what) {
     if (e != cudaSuccess) return cuda_fail(e, what);
@@ -771,7 +783,7 @@ qmm_status qmm_moe_experts(const void *x, int64_t T, int64_t K, qmm_dtype dtype,
             return fail(QMM_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
         if (g_path == QMM_PATH_DECODE_TC)
             return fail(QMM_ERR_UNSUPPORTED, "the decode tensor-core path does not take experts");
-        const bool few = g_path == QMM_PATH_GEMV || (g_path == QMM_PATH_AUTO && T * top_k <= kMoeGemvSlots);
+        const bool few = g_path == QMM_PATH_GEMV || (g_path == QMM_PATH_AUTO && moe_few_rows(a));
         if (few || (g_path == QMM_PATH_AUTO && !moe_tc_supported()))
             return finish_launch(launch_moe_gemv(dtype, a, (cudaStream_t)stream), "moe_experts launch");
         if (!moe_tc_supported())

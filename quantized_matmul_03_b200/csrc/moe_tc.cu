@@ -269,9 +269,10 @@ __device__ __forceinline__ void dequant_block(const uint32_t (&w)[8], uint32_t s
 }
 
 // Gated activation for a value that is rounded to 16 bits next.
-__device__ __forceinline__ float gate_fast(float g, int act) {
+template <int ACT>
+__device__ __forceinline__ float gate_fast(float g) {
     float z = g;
-    if (act != QMM_ACT_SILU) z = 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    if constexpr (ACT != QMM_ACT_SILU) z = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     return __fdividef(g, 1.f + __expf(-z));
 }
 
@@ -458,15 +459,20 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
                     const bool upper = lane >= 16;
                     const int f = 16 * q + (lane & 15);
                     const int pos = (f & ~7) | ((f & 3) << 1) | ((f >> 2) & 1);
-                    T *h = static_cast<T *>(p.out) + ((int64_t)nt * p.rows + ch.y) * kBK + pos;
+                    const int m0 = 32 * j + (upper ? 16 : 0), left = ch.z - m0;
+                    T *h = static_cast<T *>(p.out) + ((int64_t)nt * p.rows + ch.y + m0) * kBK + pos;
+                    auto finish = [&](auto act) {
 #pragma unroll
-                    for (int cc = 0; cc < 16; ++cc) {
-                        const float lo = __uint_as_float(v[cc]), hi = __uint_as_float(v[cc + 16]);
-                        const float got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, 16);
-                        const float gt = upper ? got : lo, up = upper ? hi : got;
-                        const int m = 32 * j + cc + (upper ? 16 : 0);
-                        if (m < ch.z) h[(int64_t)m * kBK] = Dt<T>::from_f(gate_fast(gt, p.act) * up);
-                    }
+                        for (int cc = 0; cc < 16; ++cc) {
+                            const float lo = __uint_as_float(v[cc]), hi = __uint_as_float(v[cc + 16]);
+                            const float own = upper ? hi : lo;
+                            const float got = __shfl_xor_sync(0xffffffffu, upper ? lo : hi, 16);
+                            const float r = gate_fast<decltype(act)::value>(upper ? got : own) * (upper ? own : got);
+                            if (cc < left) h[cc * kBK] = Dt<T>::from_f(r);
+                        }
+                    };
+                    if (p.act == QMM_ACT_SILU) finish(std::integral_constant<int, QMM_ACT_SILU>());
+                    else finish(std::integral_constant<int, QMM_ACT_GELU_TANH>());
                 } else {
                     const int n = nt * kBM + 32 * q + lane;
                     const int mm = 32 * j + lane;
@@ -487,8 +493,13 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
         // that had waited long for its accumulator went to the other
         // accumulator's barrier.
         if (elect_one()) {
-            uint32_t n = 0;
-            int i = 0, bslot = 0;
+            // Ring positions as running addresses: few instructions per unit,
+            // which this one thread issues one after the other.
+            const uint64_t desc0 = sw128_desc(b0);
+            const uint32_t dhi = (uint32_t)(desc0 >> 32);
+            constexpr uint32_t kStepB = BB >> 4, kEndB = kStepB * SB, kStepA = 32 * U, kEndA = kStepA * NU;
+            uint32_t bar = ready, parity = 0, aoff = 0, boff = 0;
+            int i = 0;
             for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++i) {
                 const int acc = i & 1, use = i >> 1;
                 const int4 ch = p.chunks[tile / p.n_tiles];
@@ -497,25 +508,34 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
                 if (i >= 2) wait_phase(acc_empty + 8 * acc, (use + 1) & 1, p.err);
                 tc_fence_after();
                 const uint32_t d = tmem + acc * CAP;
-                for (int ku = 0; ku < KU; ++ku, ++n) {
-                    wait_phase(ready + 8 * (n % kRing), (n / kRing) & 1, p.err);
+                uint32_t more = 0;  // whether the accumulator holds something
+                for (int left = KB; left > 0; left -= U) {
+                    wait_phase(bar, parity, p.err);
                     tc_fence_after();
-                    uint64_t db = sw128_desc(b0 + bslot * BB);
-                    uint32_t ta = tmem + a_col0 + 32u * U * (n % NU);
-                    const int blocks = min(U, KB - U * ku);
+                    uint32_t lo = (uint32_t)desc0 + boff;
+                    const uint32_t ta = tmem + a_col0 + aoff;
+                    auto block = [&](uint32_t a, uint32_t l) {
+                        auto desc = [&](uint32_t v) { return (uint64_t)dhi << 32 | v; };
+                        tc_mma_ts(d, a, desc(l), idesc, more);
+                        more = 1;
+                        tc_mma_ts(d, a + 8, desc(l + 2), idesc, 1);
+                        tc_mma_ts(d, a + 16, desc(l + 4), idesc, 1);
+                        tc_mma_ts(d, a + 24, desc(l + 6), idesc, 1);
+                    };
+                    if (left >= U) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (u < blocks) {
-                            tc_mma_ts(d, ta, db, idesc, ku != 0 || u != 0);
-                            tc_mma_ts(d, ta + 8, db + 2, idesc, 1);
-                            tc_mma_ts(d, ta + 16, db + 4, idesc, 1);
-                            tc_mma_ts(d, ta + 24, db + 6, idesc, 1);
-                        }
-                        ta += 32;
-                        db += zstep;
+                        for (int u = 0; u < U; ++u, lo += zstep) block(ta + 32 * u, lo);
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < left; ++u, lo += zstep) block(ta + 32 * u, lo);
                     }
-                    tc_commit(done + 8 * (n % kRing));
-                    if (++bslot == SB) bslot = 0;
+                    tc_commit(bar + 8 * kRing);  // done, behind ready
+                    bar += 8;
+                    if (bar == done) bar = ready, parity ^= 1;
+                    aoff += kStepA;
+                    if (aoff == kEndA) aoff = 0;
+                    boff += kStepB;
+                    if (boff == kEndB) boff = 0;
                 }
                 tc_commit(acc_full + 8 * acc);
             }

@@ -100,7 +100,7 @@ struct MoeHeader {
 };
 
 struct MoePlan {
-    size_t hdr, chunks, perm, x, h, parts, total;
+    size_t hdr, chunks, pos, x, h, parts, total;
     int64_t max_chunks;
 };
 
@@ -116,7 +116,7 @@ struct WeightMaps {
 
 struct TcParams {
     const void *scales[2], *biases[2];
-    void *out;                // h [R / 64][rows][64] T, or parts [slots][R] fp32
+    void *out;                // h [R / 64][rows][64] T, or parts [slots][R] fp32, both in sorted order
     int64_t row_bytes_sb;     // bytes of one row of scales
     int rows;                 // slots
     int R, KB, gs_log, n_tiles;
@@ -125,7 +125,6 @@ struct TcParams {
     int act;
     const MoeHeader *hdr;
     const int4 *chunks;       // {expert, first sorted row, rows, box (box_of)}
-    const int32_t *perm;
     int *err;
 };
 
@@ -475,14 +474,11 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
                     else finish(std::integral_constant<int, QMM_ACT_GELU_TANH>());
                 } else {
                     const int n = nt * kBM + 32 * q + lane;
-                    const int mm = 32 * j + lane;
-                    const int my = mm < ch.z ? p.perm[ch.y + mm] : 0;
-                    float *parts = static_cast<float *>(p.out) + n;
+                    const int left = n < p.R ? ch.z - 32 * j : 0;
+                    float *parts = static_cast<float *>(p.out) + (int64_t)(ch.y + 32 * j) * p.R + n;
 #pragma unroll
-                    for (int cc = 0; cc < 32; ++cc) {
-                        const int64_t slot = __shfl_sync(0xffffffffu, my, cc);
-                        if (32 * j + cc < ch.z && n < p.R) parts[slot * p.R] = __uint_as_float(v[cc]);
-                    }
+                    for (int cc = 0; cc < 32; ++cc, parts += p.R)
+                        if (cc < left) *parts = __uint_as_float(v[cc]);
                 }
             }
         }
@@ -659,7 +655,7 @@ struct PrepParams {
     int slots, E, cap, seg, top_k, vec;  // vec: 16-byte units of a row of x
     MoeHeader *hdr;
     int4 *chunks;
-    int32_t *perm;
+    int32_t *pos;             // sorted row of each slot, -1 without an expert
     int *err;
 };
 
@@ -763,8 +759,7 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const PrepParams
             __syncwarp();
             if (key >= 0) {
                 if (lane == __ffs(same) - 1) before[key] += __popc(same);
-                dst[i - lo] = key < E ? pos : -1;
-                if (key < E) p.perm[pos] = i;
+                dst[i - lo] = p.pos[i] = key < E ? pos : -1;
             }
             __syncwarp();
         }
@@ -808,9 +803,9 @@ __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const PrepParams
 
 // y[t] = sum over slots in order of weight * part, rounded once.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) moe_combine_kernel(const float *parts, const int32_t *indices,
+__global__ void __launch_bounds__(256) moe_combine_kernel(const float *parts, const int32_t *pos,
                                                           const float *weights, T *y, int64_t total, int N,
-                                                          int top_k, int E) {
+                                                          int top_k) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int nv = N / VEC;
@@ -827,10 +822,11 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const float *parts, co
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t slot = t * top_k + j0 + u;
-                ok[u] = j0 + u < top_k && (unsigned)indices[slot] < (unsigned)E;
+                const int row = j0 + u < top_k ? pos[slot] : -1;
+                ok[u] = row >= 0;
                 if (!ok[u]) continue;
                 w[u] = weights[slot];
-                const float *src = parts + slot * N + n;
+                const float *src = parts + (int64_t)row * N + n;
                 if constexpr (VEC == 4) {
                     const float4 f = __ldcs(reinterpret_cast<const float4 *>(src));
                     v[u][0] = f.x, v[u][1] = f.y, v[u][2] = f.z, v[u][3] = f.w;
@@ -865,7 +861,7 @@ MoePlan plan_of(const ExpertsArgs &a) {
     size_t off = 256;
     w.chunks = off;
     off += up256((size_t)w.max_chunks * sizeof(int4));
-    w.perm = off;
+    w.pos = off;
     off += up256((size_t)P * 4);
     w.x = off;
     off += up256((size_t)P * (size_t)a.K * 2);
@@ -955,7 +951,6 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) 
     p.act = a.act;
     p.hdr = reinterpret_cast<const MoeHeader *>(ws + w.hdr);
     p.chunks = reinterpret_cast<const int4 *>(ws + w.chunks);
-    p.perm = reinterpret_cast<const int32_t *>(ws + w.perm);
     p.err = device_error_word();
     auto kern = moe_tc_kernel<T, MODE, GLU, CAP>;
     struct Tag;
@@ -975,7 +970,7 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
     const int64_t P = a.T * a.top_k;
     const int cap = chunk_cap(P, a.n_experts);
     MoeHeader *hdr = reinterpret_cast<MoeHeader *>(ws + w.hdr);
-    int32_t *perm = reinterpret_cast<int32_t *>(ws + w.perm);
+    int32_t *pos = reinterpret_cast<int32_t *>(ws + w.pos);
 
     PrepParams pp{};
     pp.indices = a.indices;
@@ -988,7 +983,7 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
     pp.vec = (int)(a.K / 8);
     pp.hdr = hdr;
     pp.chunks = reinterpret_cast<int4 *>(ws + w.chunks);
-    pp.perm = perm;
+    pp.pos = pos;
     pp.err = device_error_word();
     // Two CTAs per SM, unless their stretches would be shorter than a warp's
     // share of rows or longer than shared memory holds.
@@ -1010,10 +1005,10 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
     const int cgrid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)num_sms() * 8);
     T *y = static_cast<T *>(a.y);
     if (vec4)
-        return launch_chained<moe_combine_kernel<T, 4>>(dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
-                              (int)a.N, a.top_k, (int)a.n_experts);
-    return launch_chained<moe_combine_kernel<T, 1>>(dim3(cgrid), 256, 0, s, parts, a.indices, a.weights, y, total,
-                          (int)a.N, a.top_k, (int)a.n_experts);
+        return launch_chained<moe_combine_kernel<T, 4>>(dim3(cgrid), 256, 0, s, parts, pos, a.weights, y, total,
+                              (int)a.N, a.top_k);
+    return launch_chained<moe_combine_kernel<T, 1>>(dim3(cgrid), 256, 0, s, parts, pos, a.weights, y, total,
+                          (int)a.N, a.top_k);
 }
 
 template <typename T>

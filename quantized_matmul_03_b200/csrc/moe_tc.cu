@@ -36,7 +36,7 @@
 //   5, 6   TMA of packed tiles (gate and up, or the down tile), 256 k at a time,
 //          and of their scales (and biases), a window of 16 bytes a row;
 //   7      TMA of activation tiles;
-//   8-23   dequantize, four groups of four warps; group g takes block g of each
+//   8-23   dequantize, four groups of four warps, each one or two blocks of a
 //          packed tile;
 //   24     scale windows by asynchronous copies, where a row of scales is not
 //          made of whole 16 bytes.
@@ -86,11 +86,15 @@ constexpr int kHeights[kNumHeights] = {16, 32, 64, 96, 128, 192};
 
 // Chunks of at most CAP rows: two accumulators of CAP columns leave room for NU
 // units of U dequantized k-blocks (32 columns each) in tensor memory; SB units
-// of activations lie in shared memory.
+// of activations lie in shared memory.  A dequantize group takes BPG blocks per
+// hand-over: two where the units are four blocks (32 rows x 8 of 64 experts: 84
+// us against 92 with one and 94 with four), one where two units of two are all
+// there is (2048 rows x 2 of 8: 1087 us against 1185 with two).
 template <int CAP>
 struct TileCfg {
     static constexpr int U = CAP <= 64 ? 4 : 2;
     static constexpr int NU = (512 - 2 * CAP) / (32 * U);
+    static constexpr int BPG = CAP <= 64 ? 2 : 1;  // blocks of a stage per dequantize group
     static constexpr int SB = 3;
     static constexpr int BBytes = CAP * 128 * U;
 };
@@ -323,7 +327,7 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *gbase = smem_raw + (base - raw);
     using Cfg = TileCfg<CAP>;
-    constexpr int U = Cfg::U, SB = Cfg::SB, BB = Cfg::BBytes;
+    constexpr int U = Cfg::U, BPG = Cfg::BPG, SB = Cfg::SB, BB = Cfg::BBytes;
     constexpr uint32_t NU = Cfg::NU;
     const int SP = p.SP;
     // Barriers first, then the rings: activations, packed tiles, windows.
@@ -340,10 +344,10 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
     if (threadIdx.x == 0) {
         for (int i = 0; i < SP; ++i) {
             ptx::mbar_init(full_p + 8 * i, NM + (p.sb_vec == 16 ? 0 : 32));
-            ptx::mbar_init(empty_p + 8 * i, kDqWarps);
+            ptx::mbar_init(empty_p + 8 * i, kDqWarps / BPG);
         }
         for (int i = 0; i < kRing; ++i) {
-            ptx::mbar_init(ready + 8 * i, 4 * U + 1);
+            ptx::mbar_init(ready + 8 * i, 4 * U / BPG + 1);
             ptx::mbar_init(done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -375,61 +379,68 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
         const uint8_t *prow = gbase + (p0 - base) + row * (kStageK / 2);
         const uint8_t *swin = gbase + (s0 - base) + row * 16;
         const uint32_t dst = tmem + ((uint32_t)(32 * q) << 16) + a_col0;
-        uint32_t c = 0;
+        // A group takes BPG blocks, from b0k on, of every BPG-th stage.
+        const int b0k = BPG * g % kGroups;
+        uint32_t c = 0;               // units of the tiles before
         Ring ps;
-        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
-            for (int st = 0; st < KS; ++st, ps.next(SP)) {
-                const int kb = st * kGroups + g;
+        int st = g * BPG / kGroups;
+        for (int i = 0; i < st; ++i) ps.next(SP);
+        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, st -= KS, c += KU) {
+            for (; st < KS; st += BPG) {
                 wait_phase(full_p + 8 * ps.slot, ps.phase, p.err);
-                if (kb < KB) {
-                    uint32_t w[8], sb = 0, bb = 0;
-                    const uint8_t *src = prow + ps.slot * kPBytes;
+                const uint8_t *src = prow + ps.slot * kPBytes;
+                const uint8_t *sw = swin + ps.slot * (NW * kWinBytes);
+                const int kb0 = st * kGroups + b0k;
+                const uint32_t n = c + kb0 / U;
+                const uint32_t dn = dst + 32u * U * (n % NU) + 32u * (kb0 % U);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(src + (((2 * g + i) ^ (row & 7)) << 4));
-                        w[4 * i] = u.x;
-                        w[4 * i + 1] = u.y;
-                        w[4 * i + 2] = u.z;
-                        w[4 * i + 3] = u.w;
-                    }
-                    const uint8_t *sw = swin + ps.slot * (NW * kWinBytes);
-                    if constexpr (AFF) {
-                        // first group of each half, as halves of a word
-                        const int o0 = (((kb * kBK) >> p.gs_log) * 2) & 15;
-                        const int o1 = (((kb * kBK + 32) >> p.gs_log) * 2) & 15;
-                        sb = *reinterpret_cast<const uint16_t *>(sw + o0) |
-                             ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + o1) << 16);
-                        bb = *reinterpret_cast<const uint16_t *>(sw + kWinBytes + o0) |
-                             ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + kWinBytes + o1) << 16);
-                    } else if constexpr (MODE == QMM_MODE_NVFP4) {
-                        sb = *reinterpret_cast<const uint32_t *>(sw + ((4 * kb) & 15));
-                    } else {
-                        sb = *reinterpret_cast<const uint16_t *>(sw + ((2 * kb) & 15));
-                    }
+                for (int j = 0; j < BPG; ++j) {
+                    const int kb = kb0 + j;
                     uint32_t v[32];
-                    dequant_block<T, MODE>(w, sb, bb, v);
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
-                    const uint32_t n = c + kb / U;
-                    if (n >= NU) wait_phase(done + 8 * ((n - NU) % kRing), ((n - NU) / kRing) & 1, p.err);
-                    tc_fence_after();
-                    tmem_st32(dst + 32u * U * (n % NU) + 32u * (kb % U), v);
+                    if (kb < KB) {
+                        uint32_t w[8], sb = 0, bb = 0;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(src + (((2 * (b0k + j) + i) ^ (row & 7)) << 4));
+                            w[4 * i] = u.x;
+                            w[4 * i + 1] = u.y;
+                            w[4 * i + 2] = u.z;
+                            w[4 * i + 3] = u.w;
+                        }
+                        if constexpr (AFF) {
+                            // first group of each half, as halves of a word
+                            const int o0 = (((kb * kBK) >> p.gs_log) * 2) & 15;
+                            const int o1 = (((kb * kBK + 32) >> p.gs_log) * 2) & 15;
+                            sb = *reinterpret_cast<const uint16_t *>(sw + o0) |
+                                 ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + o1) << 16);
+                            bb = *reinterpret_cast<const uint16_t *>(sw + kWinBytes + o0) |
+                                 ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + kWinBytes + o1) << 16);
+                        } else if constexpr (MODE == QMM_MODE_NVFP4) {
+                            sb = *reinterpret_cast<const uint32_t *>(sw + ((4 * kb) & 15));
+                        } else {
+                            sb = *reinterpret_cast<const uint16_t *>(sw + ((2 * kb) & 15));
+                        }
+                        dequant_block<T, MODE>(w, sb, bb, v);
+                    }
+                    if (j == BPG - 1) {
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
+                    }
+                    if (j == 0 && kb0 / U < KU && n >= NU) {
+                        wait_phase(done + 8 * ((n - NU) % kRing), ((n - NU) / kRing) & 1, p.err);
+                        tc_fence_after();
+                    }
+                    if (kb < KB) tmem_st32(dn + 32u * j, v);
+                }
+                if (kb0 / U < KU) {  // blocks missing from a tile's last unit count as there
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(ready + 8 * (n % kRing));
-                } else {
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(empty_p + 8 * ps.slot);
-                    if (kb / U < KU) {  // missing from the tile's last unit
-                        const uint32_t n = c + kb / U;
-                        if (n >= NU) wait_phase(done + 8 * ((n - NU) % kRing), ((n - NU) / kRing) & 1, p.err);
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(ready + 8 * (n % kRing));
-                    }
                 }
+#pragma unroll
+                for (int i = 0; i < BPG; ++i) ps.next(SP);
             }
-            c += KU;
         }
     } else if (warp < kMmaWarp) {
         // ------------------------- epilogue -------------------------

@@ -128,17 +128,17 @@ bool gather_tc_supported(qmm_dtype dtype, int64_t x_batch, int64_t M, int64_t K,
 
 // Whether qmm_moe_experts takes the few-row kernels.  They expand every slot's
 // expert, the tensor-core path every touched expert once, at nearly the same
-// rate (about 5.5e12 weights a second), and the latter costs about 25 us more
-// per call (sort, combine, tiles that are mostly empty): few rows while the
-// slots beyond the number of experts they are expected to touch cost less than
-// that.  Measured, few-row / tensor-core path: 4 and 6 slots over 8 experts
-// 4096 x 14336 127 / 148 and 193 / 178 us; 16 and 32 slots over 16 experts 2048
-// x 2048 53 / 57 and 94 / 74; 64 and 96 slots over 64 experts 2048 x 1024 88 /
-// 90 and 131 / 102.
+// rate (5 to 6e12 weights a second), and the latter costs about 12 us more per
+// call (sort, combine, tiles that are mostly empty): few rows while the slots
+// beyond the number of experts they are expected to touch cost less than that.
+// Measured, few-row / tensor-core path: 2 and 4 slots over 8 experts 4096 x
+// 14336 67 / 101 and 132 / 114 us; 8 and 12 slots over 16 experts 2048 x 2048
+// 34 / 42 and 46 / 43; 32 and 48 slots over 64 experts 2048 x 1024 50 / 54 and
+// 71 / 63, 1024 x 512 28 / 32 and 36 / 32.
 bool moe_few_rows(const ExpertsArgs &a) {
     const double slots = (double)a.T * a.top_k, E = (double)a.n_experts;
     const double touched = E * (1.0 - std::pow(1.0 - 1.0 / E, slots));
-    return slots <= 64 && (slots - touched) * (double)a.I * (2.0 * a.K + a.N) <= 1.4e8;
+    return slots <= 40 && (slots - touched) * (double)a.I * (2.0 * a.K + a.N) <= 6e7;
 }
 
 qmm_status finish_launch(cudaError_t e, const char *what) {

@@ -98,38 +98,39 @@ def experts(x, indices, weights, gate, up, down, mode, gs, activation, few_rows)
     """
     half = torch.finfo(x.dtype).eps / 2
     X = x.double()
+    dev = X.device
     T, K = X.shape
     E, I = gate[0].shape[:2]
     N = down[0].shape[1]
-    Wg, Wu, Wd = (dense(w, None, mode, gs) for w in (gate, up, down))
-    y = torch.zeros(T, N, dtype=torch.float64)
-    bound = torch.zeros(T, N, dtype=torch.float64)
+    y = torch.zeros(T, N, dtype=torch.float64, device=dev)
+    bound = torch.zeros(T, N, dtype=torch.float64, device=dev)
 
     def in_err(v):
         if not few_rows:
             return torch.zeros_like(v)
-        m = v.abs().reshape(-1, 32).amax(-1, keepdim=True)
-        return (m * 2.0 ** -14).expand(-1, 32).reshape(v.shape)
+        m = v.abs().reshape(v.shape[0], -1, 32).amax(-1, keepdim=True)
+        return (m * 2.0 ** -14).expand(-1, -1, 32).reshape(v.shape)
 
     wr = 2 * half if (mode == "affine" and not few_rows) else 0.0
-    for t in range(T):
-        for j in range(indices.shape[1]):
-            e = int(indices[t, j])
-            if e < 0 or e >= E:
-                continue
-            w = float(weights[t, j])
-            g, u = Wg[e] @ X[t], Wu[e] @ X[t]
-            rel = wr + K * 2.0 ** -24
-            dg = Wg[e].abs() @ in_err(X[t]) + rel * (Wg[e].abs() @ X[t].abs())
-            du = Wu[e].abs() @ in_err(X[t]) + rel * (Wu[e].abs() @ X[t].abs())
-            a = act(g, activation)
-            da = 1.13 * dg + 2.0 ** -20 * a.abs()
-            h = a * u
-            dh = da * (u.abs() + du) + a.abs() * du + 2.0 ** -23 * h.abs()
-            if not few_rows:
-                dh = dh + half * (h.abs() + dh) + torch.finfo(x.dtype).tiny
-            dh = dh + in_err(h.abs() + dh)
-            y[t] += w * (Wd[e] @ h)
-            bound[t] += abs(w) * (Wd[e].abs() @ dh + (wr + I * 2.0 ** -24) * (Wd[e].abs() @ (h.abs() + dh)))
-            bound[t] += 2.0 ** -22 * abs(w) * (Wd[e].abs() @ h.abs())
+    for e in range(E):
+        t, j = (indices == e).nonzero(as_tuple=True)
+        if t.numel() == 0:
+            continue
+        Wg, Wu, Wd = (dense(tuple(None if p is None else p[e:e + 1] for p in w), None, mode, gs)[0].to(dev)
+                      for w in (gate, up, down))
+        x_, w = X[t], weights[t, j].double()[:, None]
+        g, u = x_ @ Wg.T, x_ @ Wu.T
+        rel = wr + K * 2.0 ** -24
+        dg = in_err(x_) @ Wg.abs().T + rel * (x_.abs() @ Wg.abs().T)
+        du = in_err(x_) @ Wu.abs().T + rel * (x_.abs() @ Wu.abs().T)
+        a = act(g, activation)
+        da = 1.13 * dg + 2.0 ** -20 * a.abs()
+        h = a * u
+        dh = da * (u.abs() + du) + a.abs() * du + 2.0 ** -23 * h.abs()
+        if not few_rows:
+            dh = dh + half * (h.abs() + dh) + torch.finfo(x.dtype).tiny
+        dh = dh + in_err(h.abs() + dh)
+        part = dh @ Wd.abs().T + (wr + I * 2.0 ** -24) * ((h.abs() + dh) @ Wd.abs().T)
+        y.index_add_(0, t, w * (h @ Wd.T))
+        bound.index_add_(0, t, w.abs() * (part + 2.0 ** -22 * (h.abs() @ Wd.abs().T)))
     return y, bound + half * (y.abs() + bound) + torch.finfo(x.dtype).tiny

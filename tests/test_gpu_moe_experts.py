@@ -87,6 +87,69 @@ def test_odd_blocks_of_64(path, mode, gs):
         check(x, idx, w, ws3, mode, gs, "silu", path)
 
 
+@pytest.mark.parametrize("mode,gs", MODES)
+@pytest.mark.parametrize("T,E,K,I,N", [(40, 3, 1024, 512, 96), (700, 3, 512, 1024, 130), (650, 2, 320, 192, 200),
+                                       (395, 2, 64, 1088, 64)])
+def test_low_and_tall_chunks(mode, gs, T, E, K, I, N):
+    """Many rows per expert: chunks of every height, rows of scales in whole and in
+    broken windows, contractions of 1 to 17 blocks of 64."""
+    dtype = torch.float16 if mode == "mxfp4" else torch.bfloat16
+    if K % gs or I % gs:
+        pytest.skip("groups do not divide the contraction")
+    ws3 = layer(E, K, I, N, mode, gs, dtype, T)
+    idx, w = slots(T, 2, E, T + 1, dropped=0.2)
+    idx[: T // 3, 0] = 0                          # unequal experts
+    idx[: T // 3, 1] = -1
+    x = torch.randn((T, K), generator=torch.Generator().manual_seed(T + 2)).to(dtype)
+    check(x, idx, w, ws3, mode, gs, "silu", "gemm")
+
+
+@pytest.mark.parametrize("mode,gs,E,k,T,K,I", [("mxfp4", 32, 32, 2, 2048, 1024, 2048), ("nvfp4", 16, 8, 2, 1024, 512, 4096),
+                                               ("affine", 64, 24, 4, 200, 1024, 1024)])
+def test_many_tiles_per_block(mode, gs, E, k, T, K, I):
+    """Every thread block works through many tiles, its epilogue behind its MMAs."""
+    ws3 = layer(E, K, I, K, mode, gs, torch.bfloat16, E)
+    idx, w = slots(T, k, E, T)
+    x = torch.randn((T, K), generator=torch.Generator().manual_seed(T)).bfloat16()
+    dev = tuple(map(cu, ws3))
+    ref, bound = moe_ref.experts(x.cuda(), idx.cuda(), w.cuda(), *ws3, mode, gs, "silu", few_rows=False)
+    first = None
+    for _ in range(3):
+        y = run(x, idx, w, dev, mode, gs, path="gemm")
+        assert bool(((y.double() - ref).abs() <= bound).all())
+        first = y if first is None else first
+        assert torch.equal(first, y)
+
+
+@pytest.mark.parametrize("mode,gs", [("mxfp4", 32), ("affine", 128)])
+@pytest.mark.parametrize("K,I", [(17408, 64), (128, 17408), (20544, 128)])
+def test_long_contractions_of_the_few_row_path(mode, gs, K, I):
+    """More segments than the streamed kernel holds results for."""
+    if K % gs or I % gs:
+        pytest.skip("groups do not divide the contraction")
+    ws3 = layer(2, K, I, 70, mode, gs, torch.bfloat16, K)
+    idx, w = slots(3, 2, 2, I)
+    x = torch.randn((3, K), generator=torch.Generator().manual_seed(I)).bfloat16()
+    check(x, idx, w, ws3, mode, gs, "silu", "gemv")
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_most_experts(path):
+    E, k = 1024, 8
+    ws3 = layer(E, 64, 64, 40, "mxfp4", 32, torch.bfloat16, 22)
+    idx, w = slots(60, k, E, 23)
+    x = torch.randn((60, 64), generator=torch.Generator().manual_seed(24)).bfloat16()
+    check(x, idx, w, ws3, "mxfp4", 32, "silu", path)
+
+
+def test_automatic_path_is_one_of_the_two():
+    ws3 = layer(8, 512, 512, 256, "mxfp4", 32, torch.bfloat16, 25)
+    for T, path in ((1, "gemv"), (200, "gemm")):
+        idx, w = slots(T, 2, 8, T)
+        x = torch.randn((T, 512), generator=torch.Generator().manual_seed(T)).bfloat16()
+        assert torch.equal(run(x, idx, w, ws3, "mxfp4", 32), run(x, idx, w, ws3, "mxfp4", 32, path=path))
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_slots_left_out(path):
     ws3 = layer(4, 128, 128, 64, "mxfp4", 32, torch.bfloat16, 3)

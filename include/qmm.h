@@ -414,7 +414,7 @@ qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t T, int64_t
  *   twice for one token; both slots count.
  * Rounding: sums are fp32 or exact integers, and y is rounded once.  With few
  *   rows (and under QMM_PATH_GEMV) activations enter as 16-bit integers per 32
- *   elements (error at most 2^-15 of their largest) and h stays fp32; with more
+ *   elements (error at most 2^-14 of their largest) and h stays fp32; with more
  *   rows (and under QMM_PATH_GEMM) h is rounded to `dtype`, the tensor cores'
  *   operand, and so is each weight of the "affine" mode and of "nvfp4" and
  *   "mxfp4" where X * element is no `dtype` value (never for normal ones).

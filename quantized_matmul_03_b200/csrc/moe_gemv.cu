@@ -13,15 +13,15 @@
 // Arithmetic.  32 activations are held as 16-bit integers over a common power
 // of two (error at most 2^-14 of the largest of the 32), codes are small
 // integers, and DP2A sums their products exactly: 4-bit affine codes as they
-// are, E2M1 codes doubled (an integer in [-12, 12]) and offset by 128, which
-// -128 sum(x_int) takes out again.  The integer sum is scaled by the group's
+// are, E2M1 codes doubled (an integer in [-12, 12]) and offset by 64, which
+// -64 sum(x_int) takes out again.  The integer sum is scaled by the group's
 // scale in fp32.  Between the kernels h stays in fp32.
 //
 // Every code is read once per slot.  Two forms of each kernel: weights streamed
 // through shared memory by bulk copies (moe_stream_kernel), and, for shapes that
 // those cannot take, loaded 16 bytes per lane with two batches of eight loads in
 // flight per warp (moe_gemv_kernel).  One token, 2 of 8 experts 4096 x 14336
-// mxfp4, 187 MB: 58 us (3.2 TB/s; 69 us with plain loads); 8 of 64 experts 2048
+// mxfp4, 187 MB: 56 us (3.3 TB/s; 69 us with plain loads); 8 of 64 experts 2048
 // x 1024 nvfp4, 28 MB: 22 us.  Bound: the two launches with their ring's first
 // and last stages, and between them the consumer warps' instructions.
 #include "moe.cuh"
@@ -93,17 +93,38 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
     return v;
 }
 
-// Eight E2M1 codes as unsigned bytes 128 + 2 e, four per word: a byte
-// permutation of the table of doubled magnitudes by the raw nibbles gives the
-// magnitude of every non-negative code and 0 for a negative one (selector bit
-// 3 asks for the sign of a table byte), by the nibbles with their sign bits
-// flipped the converse; 128 + pos - neg cannot borrow between bytes.
-// A, B: the table, held in registers by the caller (as constants they were
-// set up again before every permutation).
-__device__ __forceinline__ void e2m1_bytes(uint32_t A, uint32_t B, uint32_t w, uint32_t &lo, uint32_t &hi) {
+// Constants of the E2M1 decoding, held in registers (as literals they were set
+// up again before every permutation, or turned a multiplication back into an
+// instruction of the integer pipe).
+struct E2m1Table {
+    uint32_t pa, pb;   // 64 + 2 e of codes 0..7, a byte each
+    uint32_t na, nb;   // 64 - 2 e
+    uint32_t one;
+    __device__ __forceinline__ void set() {
+        asm volatile("mov.u32 %0, 0x43424140;" : "=r"(pa));
+        asm volatile("mov.u32 %0, 0x4C484644;" : "=r"(pb));
+        asm volatile("mov.u32 %0, 0x3D3E3F40;" : "=r"(na));
+        asm volatile("mov.u32 %0, 0x34383A3C;" : "=r"(nb));
+        asm volatile("mov.u32 %0, 1;" : "=r"(one));
+    }
+};
+__device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// Eight E2M1 codes as unsigned bytes 64 + 2 e, four per word: a byte
+// permutation of the first table by the raw nibbles gives the byte of every
+// non-negative code and 0 for a negative one (selector bit 3 asks for the sign
+// of a table byte), of the second by the nibbles with their sign bits flipped
+// the converse.  The integer pipe is the kernel's busiest: their sum goes to the
+// multiply pipe (one token, 2 of 8 experts 4096 x 14336: 63 us, 65.5 with
+// integer additions).
+__device__ __forceinline__ void e2m1_bytes(const E2m1Table &t, uint32_t w, uint32_t &lo, uint32_t &hi) {
     const uint32_t n = w ^ 0x88888888u;
-    lo = prmt(A, B, w) + 0x80808080u - prmt(A, B, n);
-    hi = prmt(A, B, w >> 16) + 0x80808080u - prmt(A, B, n >> 16);
+    lo = mad(prmt(t.pa, t.pb, w), t.one, prmt(t.na, t.nb, n));
+    hi = mad(prmt(t.pa, t.pb, w >> 16), t.one, prmt(t.na, t.nb, n >> 16));
 }
 
 // A lane's 32 activations: pairs of 16-bit integers in the order in which DP2A
@@ -113,8 +134,8 @@ struct Slice {
     int x[16];
     float unit;      // 2^-sh (E2M1: half of it, the codes being doubled); NaN if any activation is infinite or NaN
     float xsum;      // affine: sum of the activations
-    int off[2];      // E2M1: -128 * sum of the integers of each half
-    uint32_t ta, tb; // E2M1: doubled magnitudes of codes 0..7, a byte each
+    int off[2];      // E2M1: -64 * sum of the integers of each half
+    E2m1Table e2m1;
 };
 
 // Element of half h (0, 1) of pair k within a word of eight codes.  Affine
@@ -153,8 +174,7 @@ __device__ __forceinline__ void load_slice(const X *x, bool ok, float (&f)[32]) 
 
 template <int MODE>
 __device__ __forceinline__ void make_slice(const float (&f)[32], Slice &s) {
-    asm volatile("mov.u32 %0, 0x03020100;" : "=r"(s.ta));
-    asm volatile("mov.u32 %0, 0x0C080604;" : "=r"(s.tb));
+    if constexpr (MODE != QMM_MODE_AFFINE) s.e2m1.set();
     uint32_t mb = 0;  // largest |x| by bit pattern (infinities and NaN largest)
 #pragma unroll
     for (int i = 0; i < 32; ++i) mb = max(mb, __float_as_uint(f[i]) & 0x7FFFFFFFu);
@@ -182,10 +202,10 @@ __device__ __forceinline__ void make_slice(const float (&f)[32], Slice &s) {
     s.xsum = s.unit * (float)(s0 + s1);
     if constexpr (MODE != QMM_MODE_AFFINE) s.unit *= 0.5f;
     if constexpr (MODE == QMM_MODE_NVFP4) {
-        s.off[0] = -128 * s0;
-        s.off[1] = -128 * s1;
+        s.off[0] = -64 * s0;
+        s.off[1] = -64 * s1;
     } else {
-        s.off[0] = -128 * (s0 + s1);
+        s.off[0] = -64 * (s0 + s1);
         s.off[1] = 0;
     }
 }
@@ -217,7 +237,7 @@ __device__ __forceinline__ float dot_slice(const Slice &s, const uint4 &w, uint3
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t lo, hi;
-            e2m1_bytes(s.ta, s.tb, ws[i], lo, hi);
+            e2m1_bytes(s.e2m1, ws[i], lo, hi);
             int &c0 = (NV && i >= 2) ? b0 : a0;
             int &c1 = (NV && i >= 2) ? b1 : a1;
             c0 = dp2a_lo(s.x[4 * i], lo, c0);

@@ -488,9 +488,11 @@ def qmm_moe_route(logits, top_k: int, score: str = "softmax", bias: Optional[tor
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != E or bias.device != device):
         raise ValueError(f"bias must hold {E} float32 values on the logits' device")
     if out is None:
-        shape = (*shape[:-1], top_k)
-        indices = torch.empty(shape, dtype=torch.int32, device=device)
-        weights = torch.empty(shape, dtype=torch.float32, device=device)
+        # (the cheapest two allocations; the call's host time is what a small batch takes)
+        indices = torch.empty_strided((T, top_k), (top_k, 1), dtype=torch.int32, device=device)
+        if len(shape) != 2:
+            indices = indices.view(*shape[:-1], top_k)
+        weights = torch.empty_like(indices, dtype=torch.float32)
     else:
         indices, weights = out
         _cuda(indices, weights)

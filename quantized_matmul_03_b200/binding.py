@@ -524,35 +524,40 @@ def qmm_moe_experts(x, indices, weights, gate, up, down, group_size: int = 64, b
     them for weights [n_experts, I, K], [n_experts, I, K], [n_experts, N, I].
     ``workspace``: a uint8 tensor of qmm_moe_experts_workspace_size(...) bytes to
     use (one per call in flight), or None to allocate one."""
-    tensors = [x, indices, weights, *gate, *up, *down, workspace, out]
-    _cuda(*tensors)
-    if any(t is not None and t.device != x.device for t in tensors):
-        raise ValueError("every tensor must be on x's device")
+    # (a decode step's layer takes about as long as these checks: one pass over the tensors)
+    dev = x.get_device()
+    for t in (x, indices, weights, *gate, *up, *down, workspace, out):
+        if t is not None:
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("libqmm takes contiguous CUDA tensors")
+            if t.get_device() != dev:
+                raise ValueError("every tensor must be on x's device")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
     if indices.dtype != torch.int32 or weights.dtype != torch.float32:
         raise ValueError("indices must be int32 and weights float32")
-    K = x.shape[-1]
+    shape, slots = x.shape, indices.shape
+    K, top_k = shape[-1], slots[-1]
     T = x.numel() // K if K else 0
-    top_k = indices.shape[-1]
-    if indices.shape != weights.shape or indices.numel() != T * top_k:
+    if slots != weights.shape or indices.numel() != T * top_k:
         raise ValueError(f"indices and weights must be [{T}, top_k]")
     for w in (gate, up, down):
         if w[0].dim() != 3 or w[0].dtype != torch.int32 or w[1].dim() != 3:
             raise ValueError("expert weights are stacked [n_experts, rows, words] int32 with scales [n_experts, rows, groups]")
-    n_experts, I = gate[0].shape[0], gate[0].shape[1]
+    n_experts, I, _ = gate[0].shape
     N = down[0].shape[1]
     if mode not in MX_MODES and mode != "affine":
         raise ValueError(f"unknown mode {mode}")
     sdt = torch.uint8 if mode in MX_MODES else x.dtype
     for name, w, rows, cols in (("gate", gate, I, K), ("up", up, I, K), ("down", down, N, I)):
-        if tuple(w[0].shape) != (n_experts, rows, cols * bits // 32):
+        if w[0].shape != (n_experts, rows, cols * bits // 32):
             raise ValueError(f"{name}: packed weight must be {(n_experts, rows, cols * bits // 32)}")
+        groups = (n_experts, rows, cols // group_size)
         for s in w[1:]:
-            if s is not None and (tuple(s.shape) != (n_experts, rows, cols // group_size) or s.dtype != sdt):
-                raise ValueError(f"{name}: scales and biases must be {(n_experts, rows, cols // group_size)} {sdt}")
+            if s is not None and (s.shape != groups or s.dtype != sdt):
+                raise ValueError(f"{name}: scales and biases must be {groups} {sdt}")
     if out is None:
-        out = torch.empty(tuple(x.shape[:-1]) + (N,), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if N == K else torch.empty((*shape[:-1], N), dtype=x.dtype, device=x.device)
     elif out.dtype != x.dtype or out.numel() != T * N:
         raise ValueError(f"out must hold {T} x {N} values of {x.dtype}")
     with _on(x.device):

@@ -657,7 +657,7 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
 // Preparation: slots sorted by expert, chunks, the copy of x.
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 512, kPrepWarps = kPrepThreads / 32;
-constexpr int kPrepSeg = 1024;  // slots of a CTA at most
+constexpr int kPrepSeg = 8192;  // slots of a CTA at most
 
 struct PrepParams {
     const int32_t *indices;
@@ -722,9 +722,9 @@ __device__ __forceinline__ int box_of(int rows) {
 __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const PrepParams p) {
     extern __shared__ int sm[];
     __shared__ int tmp[kPrepWarps];
-    __shared__ int dst[kPrepSeg];  // sorted row of each slot of the stretch, -1 without an expert
     const int E = p.E;
     int *first = sm, *before = first + E + 2, *nch = before + E + 1;
+    int *dst = nch + E + 1;  // sorted row of each slot of the stretch, -1 without an expert
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < 2 * E + 3; i += kPrepThreads) sm[i] = 0;
     __syncthreads();
@@ -936,7 +936,7 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) 
     const uint64_t dims[3] = {64, (uint64_t)P, (uint64_t)C / 64};
     // x rows as they are ([slots][K], k-blocks 128 bytes apart); h by k-blocks
     const uint64_t strides[2] = {GLU ? (uint64_t)C * 2 : 128, GLU ? 128 : (uint64_t)P * 128};
-    for (int i = 0; i < kNumHeights; ++i) {
+    for (int i = 0; i < kNumHeights && kHeights[i] <= CAP; ++i) {
         const uint32_t box[3] = {64, (uint32_t)kHeights[i], (uint32_t)Cfg::U};
         if (!make_map(&mb.m[i], std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -999,7 +999,7 @@ cudaError_t run_tc(const ExpertsArgs &a, cudaStream_t s) {
     // Two CTAs per SM, unless their stretches would be shorter than a warp's
     // share of rows or longer than shared memory holds.
     pp.seg = (int)std::min<int64_t>(kPrepSeg, std::max<int64_t>(8, (P + 2 * num_sms() - 1) / (2 * num_sms())));
-    const size_t smem = (size_t)(3 * (pp.E + 2)) * sizeof(int);
+    const size_t smem = (size_t)(3 * pp.E + 4 + pp.seg) * sizeof(int);  // 46 KB at most
     cudaError_t e = launch_chained<moe_prep_kernel>(dim3((unsigned)((P + pp.seg - 1) / pp.seg)), kPrepThreads, smem, s, pp);
     if (e != cudaSuccess) return e;
     if (cap <= 64) {

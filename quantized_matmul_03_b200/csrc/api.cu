@@ -138,7 +138,7 @@ bool gather_tc_supported(qmm_dtype dtype, int64_t x_batch, int64_t M, int64_t K,
 bool moe_few_rows(const ExpertsArgs &a) {
     const double slots = (double)a.T * a.top_k, E = (double)a.n_experts;
     const double touched = E * (1.0 - std::pow(1.0 - 1.0 / E, slots));
-    return slots <= 40 && (slots - touched) * (double)a.I * (2.0 * a.K + a.N) <= 6e7;
+    return moe_gemv_supported(a) && slots <= 40 && (slots - touched) * (double)a.I * (2.0 * a.K + a.N) <= 6e7;
 }
 
 qmm_status finish_launch(cudaError_t e, const char *what) {
@@ -784,7 +784,9 @@ qmm_status qmm_moe_experts(const void *x, int64_t T, int64_t K, qmm_dtype dtype,
         if (g_path == QMM_PATH_DECODE_TC)
             return fail(QMM_ERR_UNSUPPORTED, "the decode tensor-core path does not take experts");
         const bool few = g_path == QMM_PATH_GEMV || (g_path == QMM_PATH_AUTO && moe_few_rows(a));
-        if (few || (g_path == QMM_PATH_AUTO && !moe_tc_supported()))
+        if (g_path == QMM_PATH_GEMV && !moe_gemv_supported(a))
+            return fail(QMM_ERR_UNSUPPORTED, "the few-row path does not take contractions this long");
+        if (few || (g_path == QMM_PATH_AUTO && !moe_tc_supported() && moe_gemv_supported(a)))
             return finish_launch(launch_moe_gemv(dtype, a, (cudaStream_t)stream), "moe_experts launch");
         if (!moe_tc_supported())
             return fail(QMM_ERR_UNSUPPORTED, "the tensor-core path needs the driver's tensor maps");

@@ -47,7 +47,10 @@ struct ExpertsArgs {
 // Bytes any path of qmm_moe_experts needs for these sizes.
 size_t moe_experts_workspace(const ExpertsArgs &a);
 // Few rows: two kernels that stream each slot's expert once per slot; more
-// tokens than one pass takes go through in blocks.
+// tokens than one pass takes go through in blocks.  Supported where a token's
+// partial sums of one row fit a CTA's share of shared memory (contractions up to
+// 393216 with 32 slots per token).
+bool moe_gemv_supported(const ExpertsArgs &a);
 size_t moe_gemv_workspace(const ExpertsArgs &a);
 cudaError_t launch_moe_gemv(qmm_dtype dt, const ExpertsArgs &a, cudaStream_t s);
 // Many rows: sort by expert and two grouped tensor-core products.

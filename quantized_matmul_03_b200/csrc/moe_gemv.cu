@@ -613,10 +613,9 @@ cudaError_t launch_half(GemvParams p, cudaStream_t s) {
     p.unit_warps = std::min(p.units, kMaxWarps);
     p.row_splits = kMaxWarps / p.unit_warps;
     int64_t rows = (p.R + num_sms() - 1) / num_sms();
-    rows = std::min<int64_t>(rows, std::max<int64_t>(1, kPartBytes / ((int64_t)p.units * NM * 4)));
+    rows = std::min<int64_t>(rows, kPartBytes / ((int64_t)p.units * NM * 4));
     p.rows_cta = (int)rows;
     const size_t smem = (size_t)p.units * (size_t)rows * NM * 4;
-    if (smem > 200 * 1024) return cudaErrorInvalidConfiguration;
     auto kern = moe_gemv_kernel<T, X, MODE, GLU>;
     struct Tag;
     cudaError_t e = configure_once<Tag>(smem, [&]() {
@@ -677,6 +676,10 @@ int64_t block_tokens(const ExpertsArgs &a) {
 }
 
 }  // namespace
+
+bool moe_gemv_supported(const ExpertsArgs &a) {
+    return a.top_k * ((std::max(a.K, a.I) + kSeg - 1) / kSeg) * 8 <= kPartBytes;
+}
 
 size_t moe_gemv_workspace(const ExpertsArgs &a) {
     return (size_t)(std::min<int64_t>(a.T, block_tokens(a)) * a.top_k) * (size_t)a.I * 4;

@@ -133,6 +133,22 @@ def test_long_contractions_of_the_few_row_path(mode, gs, K, I):
     check(x, idx, w, ws3, mode, gs, "silu", "gemv")
 
 
+def test_contraction_past_the_few_row_path():
+    """32 slots of one token over a contraction whose partial sums the few-row
+    kernels have no room for: refused there, taken by the automatic path."""
+    K, k = 393216 + 1024, 32
+    g = torch.Generator().manual_seed(26)
+    wq = [torch.randint(-2 ** 31, 2 ** 31 - 1, s, generator=g, dtype=torch.int64).to(torch.int32)
+          for s in ((1, 64, K // 8), (1, 64, K // 8), (1, 64, 8))]
+    ws3 = tuple((q, torch.full((1, 64, q.shape[2] // 4), 118, dtype=torch.uint8), None) for q in wq)
+    idx, w = torch.zeros((1, k), dtype=torch.int32), torch.rand((1, k), generator=g) + 0.1
+    x = (torch.randn((1, K), generator=g) * 2.0 ** -6).bfloat16()
+    with pytest.raises(qb.QmmError) as e:
+        run(x, idx, w, ws3, "mxfp4", 32, path="gemv")
+    assert e.value.status == 2
+    check(x, idx, w, ws3, "mxfp4", 32, "silu", "auto")
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_most_experts(path):
     E, k = 1024, 8

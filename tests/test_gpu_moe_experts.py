@@ -253,6 +253,32 @@ def test_scales_far_from_one(path, dtype, mode, gs):
     check(x, idx, wt, ws3, mode, gs, "silu", path)
 
 
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("gs", [32, 128])
+def test_affine_scales_of_every_size(path, dtype, gs):
+    """Scales of both signs from 2^-12 to 2^2, and zero, beside each other in a row.
+    (Biases keep the weights among the normal f16 values, where a rounding is
+    relative to the weight.)"""
+    E, K, I, N = 2, 256, 128, 48
+    g = torch.Generator().manual_seed(27)
+
+    def w(rows, cols):
+        wq = torch.randint(-2 ** 31, 2 ** 31 - 1, (E, rows, cols // 8), generator=g, dtype=torch.int64).to(torch.int32)
+        s = torch.exp2(torch.randint(-12, 3, (E, rows, cols // gs), generator=g).float()) * (1 + torch.rand((E, rows, cols // gs), generator=g))
+        s = torch.where(torch.rand(s.shape, generator=g) < 0.5, -s, s)
+        s[torch.rand(s.shape, generator=g) < 0.05] = 0.0
+        b = torch.where(s < 0, -1.0, 1.0) * (2.0 ** -9 + torch.rand(s.shape, generator=g) * 2.0 ** -3)
+        return wq, s.to(dtype), b.to(dtype)
+
+    ws3 = (w(I, K), w(I, K), w(N, I))
+    x = (torch.randn((6, K), generator=g) * 2.0 ** -9).to(dtype)
+    idx, wt = slots(6, 2, 2, 28)
+    ref, _ = moe_ref.experts(x, idx, wt, *ws3, "affine", gs, "silu", few_rows=False)
+    assert float(ref.abs().max()) < torch.finfo(dtype).max / 4
+    check(x, idx, wt, ws3, "affine", gs, "silu", path)
+
+
 def test_token_block_of_the_few_row_path():
     """More slots than one pass of the few-row kernels takes."""
     ws3 = layer(5, 128, 192, 33, "nvfp4", 16, torch.float16, 11)

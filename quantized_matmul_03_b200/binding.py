@@ -525,10 +525,10 @@ def qmm_moe_experts(x, indices, weights, gate, up, down, group_size: int = 64, b
     ``workspace``: a uint8 tensor of qmm_moe_experts_workspace_size(...) bytes to
     use (one per call in flight), or None to allocate one."""
     # (a decode step's layer takes about as long as these checks: one pass over the tensors)
-    dev = x.get_device()
+    dev = x.get_device()  # (-1: not on a CUDA device)
     for t in (x, indices, weights, *gate, *up, *down, workspace, out):
         if t is not None:
-            if not t.is_cuda or not t.is_contiguous():
+            if dev < 0 or not t.is_contiguous():
                 raise ValueError("libqmm takes contiguous CUDA tensors")
             if t.get_device() != dev:
                 raise ValueError("every tensor must be on x's device")

@@ -50,10 +50,11 @@
 //
 // Bound: with few rows per expert the dequantize warps' instructions (about 3
 // per element), with many rows the tensor cores and, on short contractions, the
-// epilogue.  2048 rows, 8 experts 4096 x 14336, 2 each, nvfp4: gate/up 706 us,
-// down 417 us (1.29e15 operations a second); 512 rows: 241 and 170 us.  Two CTAs
+// epilogue.  2048 rows, 8 experts 4096 x 14336, 2 each, nvfp4: gate/up 645 us,
+// down 416 us (1.36e15 operations a second); 512 rows: 230 and 165 us.  Two CTAs
 // sharing an activation tile (MMAs of 256 rows) measured 741 and 446, 292 and
-// 200 us: the hand-overs between the two cost more than the halved copies save.
+// 200 us where one measured 777 and 465, 273 and 191: the hand-overs between the
+// two cost what the halved copies save.
 #include <cuda.h>
 
 #include <algorithm>

@@ -38,8 +38,9 @@
 //   7      TMA of activation tiles;
 //   8-23   dequantize, four groups of four warps, each one or two blocks of a
 //          packed tile;
-//   24     scale windows by asynchronous copies, where a row of scales is not
-//          made of whole 16 bytes.
+//   24     scale windows by asynchronous copies of 32 bytes a row, where a row of
+//          scales is not made of whole 16 bytes (300 rows x 3 of 10 experts 4160
+//          x 4160 mxfp4: 160 us, 255 with loads of 2 bytes).
 // Three rings: packed tiles and windows, activation tiles, and dequantized
 // blocks in tensor memory.  A barrier's hand-over costs its waiter 150 cycles
 // and more even when it need not wait, an MMA 40 and a TMA 200 cycles of their
@@ -78,7 +79,6 @@ constexpr int kThreads = 32 * (kSWarp + 1);
 constexpr int kBM = 128, kBK = 64;
 constexpr int kStageK = kBK * kGroups;    // k per packed stage
 constexpr int kPBytes = kBM * kStageK / 2;  // 16 KB
-constexpr int kWinBytes = kBM * 16;       // one window of 16 bytes per row
 constexpr int kRing = 8;                  // hand-over barriers (more than units in flight)
 constexpr int kBarBytes = 1024;           // barriers and the tensor-memory address
 constexpr int kMaxCap = 192;              // activation rows of a tile at most
@@ -126,7 +126,8 @@ struct TcParams {
     int rows;                 // slots
     int R, KB, gs_log, n_tiles;
     int SP;                   // packed stages
-    int sb_vec;               // scale windows by TMA (16), or by copies of 4 or 2 bytes
+    int win;                  // bytes of a row's scale window: 16 (by TMA) or 32
+    int64_t bytes_sb;         // bytes of all scales of a stack
     int act;
     const MoeHeader *hdr;
     const int4 *chunks;       // {expert, first sorted row, rows, box (box_of)}
@@ -311,8 +312,9 @@ __device__ __forceinline__ float gate_fast(float g) {
     return __fdividef(g, 1.f + __expf(-z));
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes, of which the first n are read and the rest are zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 // Arrive on bar once this thread's cp.async so far have landed (counted among
 // the barrier's arrivals).
@@ -345,7 +347,7 @@ struct Ring {
     }
 };
 
-template <typename T, int MODE, bool GLU, int CAP>
+template <typename T, int MODE, bool GLU, int CAP, int WIN>
 __global__ void __launch_bounds__(kThreads, 1)
 moe_tc_kernel(const __grid_constant__ WeightMaps maps,
               const __grid_constant__ ActMaps map_b, const __grid_constant__ TcParams p) {
@@ -361,6 +363,7 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
     using Cfg = TileCfg<CAP>;
     constexpr int U = Cfg::U, BPG = Cfg::BPG, SB = Cfg::SB, BB = Cfg::BBytes;
     constexpr uint32_t NU = Cfg::NU;
+    constexpr int win_bytes = kBM * WIN;  // scale windows of a stage (and as many of biases)
     const int SP = p.SP;
     // Barriers first, then the rings: activations, packed tiles, windows.
     const uint32_t bars = base, b0 = base + kBarBytes, p0 = b0 + SB * BB, s0 = p0 + SP * kPBytes;
@@ -375,7 +378,7 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < SP; ++i) {
-            ptx::mbar_init(full_p + 8 * i, NM + (p.sb_vec == 16 ? 0 : 32));
+            ptx::mbar_init(full_p + 8 * i, NM + (WIN == 16 ? 0 : 32));
             ptx::mbar_init(empty_p + 8 * i, kDqWarps / BPG);
         }
         for (int i = 0; i < kRing; ++i) {
@@ -409,7 +412,8 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
         const int g = (warp - kDqWarp) >> 2, q = warp & 3;
         const int row = GLU ? 16 * q + (lane & 15) + ((lane & 16) << 2) : 32 * q + lane;
         const uint8_t *prow = gbase + (p0 - base) + row * (kStageK / 2);
-        const uint8_t *swin = gbase + (s0 - base) + row * 16;
+        const uint8_t *swin = gbase + (s0 - base) + row * WIN;
+        uint32_t shift = 0;           // where the row's window begins in its 32 bytes
         const uint32_t dst = tmem + ((uint32_t)(32 * q) << 16) + a_col0;
         // A group takes BPG blocks, from b0k on, of every BPG-th stage.
         const int b0k = BPG * g % kGroups;
@@ -418,10 +422,14 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
         int st = g * BPG / kGroups;
         for (int i = 0; i < st; ++i) ps.next(SP);
         for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, st -= KS, c += KU) {
+            if constexpr (WIN != 16) {
+                const uint32_t n = (tile % p.n_tiles) * (kBM / NM) + (GLU ? row & 63 : row);
+                shift = ((uint32_t)p.chunks[tile / p.n_tiles].x * p.R + n) * (uint32_t)p.row_bytes_sb & 15u;
+            }
             for (; st < KS; st += BPG) {
                 wait_phase(full_p + 8 * ps.slot, ps.phase, p.err);
                 const uint8_t *src = prow + ps.slot * kPBytes;
-                const uint8_t *sw = swin + ps.slot * (NW * kWinBytes);
+                const uint8_t *sw = swin + ps.slot * (NW * win_bytes) + shift;
                 const int kb0 = st * kGroups + b0k;
                 const uint32_t n = c + kb0 / U;
                 const uint32_t dn = dst + 32u * U * (n % NU) + 32u * (kb0 % U);
@@ -445,8 +453,8 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
                             const int o1 = (((kb * kBK + 32) >> p.gs_log) * 2) & 15;
                             sb = *reinterpret_cast<const uint16_t *>(sw + o0) |
                                  ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + o1) << 16);
-                            bb = *reinterpret_cast<const uint16_t *>(sw + kWinBytes + o0) |
-                                 ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + kWinBytes + o1) << 16);
+                            bb = *reinterpret_cast<const uint16_t *>(sw + win_bytes + o0) |
+                                 ((uint32_t)*reinterpret_cast<const uint16_t *>(sw + win_bytes + o1) << 16);
                         } else if constexpr (MODE == QMM_MODE_NVFP4) {
                             sb = *reinterpret_cast<const uint32_t *>(sw + ((4 * kb) & 15));
                         } else {
@@ -588,9 +596,9 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
         const int m = warp - kWWarp;
         if (lane == 0 && m < NM) {
             const CUtensorMap *map = &maps.w[m];
-            constexpr uint32_t bytes = kPBytes / NM, sbytes = kWinBytes / NM;
+            constexpr uint32_t bytes = kPBytes / NM, sbytes = kBM * 16 / NM;
             constexpr int ES = AFF ? 2 : 1;
-            const bool windows = p.sb_vec == 16;
+            const bool windows = WIN == 16;
             const uint32_t total = bytes + (windows ? NW * sbytes : 0u);
             Ring ps;
             int n = 0;
@@ -604,9 +612,9 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
                                 full_p + 8 * ps.slot);
                     if (windows) {
                         const int at = (((st * kStageK) >> p.gs_log) * ES & ~15) / ES;
-                        const uint32_t win = s0 + ps.slot * (NW * kWinBytes) + m * sbytes;
+                        const uint32_t win = s0 + ps.slot * (NW * win_bytes) + m * sbytes;
                         tma_load_2d(win, &maps.s[m], at, r0, full_p + 8 * ps.slot);
-                        if constexpr (AFF) tma_load_2d(win + kWinBytes, &maps.b[m], at, r0, full_p + 8 * ps.slot);
+                        if constexpr (AFF) tma_load_2d(win + win_bytes, &maps.b[m], at, r0, full_p + 8 * ps.slot);
                     }
                 }
             }
@@ -633,46 +641,41 @@ moe_tc_kernel(const __grid_constant__ WeightMaps maps,
             for (uint32_t k = n < (uint32_t)SB ? 0 : n - SB; k < n; ++k)
                 ptx::mbar_drain(ready + 8 * (k % kRing), (k / kRing) & 1, p.err);
         }
-    } else if (p.sb_vec != 16) {
+    } else if (WIN != 16) {
         // ------------------------- scale windows -------------------------
+        // Rows of scales that are not whole 16 bytes begin anywhere: the two
+        // aligned 16-byte pieces that hold a row's window (the stack's first
+        // byte is aligned), nothing past the stack's end.
         constexpr int ES = AFF ? 2 : 1;
         Ring ps;
         for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
             const int4 ch = p.chunks[tile / p.n_tiles];
             const int nt = tile % p.n_tiles;
-            const uint8_t *src[4][NW];
-            bool ok[4];
+            int64_t off[4];  // row's first byte, or past the end: not read
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = lane + 32 * i;
-                const int m = GLU ? i >> 1 : 0;
                 const int n = GLU ? nt * (kBM / 2) + (r & 63) : nt * kBM + r;
-                ok[i] = n < p.R;  // rows past the last expert's end are not read
-                const int64_t off = ((int64_t)ch.x * p.R + n) * p.row_bytes_sb;
-                src[i][0] = static_cast<const uint8_t *>(p.scales[m]) + off;
-                if constexpr (AFF) src[i][1] = static_cast<const uint8_t *>(p.biases[m]) + off;
+                off[i] = n < p.R ? ((int64_t)ch.x * p.R + n) * p.row_bytes_sb : p.bytes_sb;
             }
             for (int st = 0; st < KS; ++st, ps.next(SP)) {
                 if (ps.wrapped) wait_phase(empty_p + 8 * ps.slot, ps.phase ^ 1, p.err);
-                const uint32_t win = s0 + ps.slot * (NW * kWinBytes) + lane * 16;
+                const uint32_t win = s0 + ps.slot * (NW * win_bytes) + lane * 32;
                 const int64_t at = (((int64_t)st * kStageK) >> p.gs_log) * ES & ~15;  // window's first byte
-                const int left = (int)min((int64_t)16, p.row_bytes_sb - at);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (!ok[i]) continue;
+                    const int64_t from = (off[i] + at) & ~(int64_t)15;
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
-                        const uint32_t d = win + w * kWinBytes + i * 512;
-                        if (p.sb_vec == 4) {
-                            for (int o = 0; o < left; o += 4) cp_async4(d + o, src[i][w] + at + o);
-                        } else {
-                            for (int o = 0; o < left; o += 2)
-                                sts16(d + o, __ldg(reinterpret_cast<const uint16_t *>(src[i][w] + at + o)));
-                        }
+                        const uint8_t *src = static_cast<const uint8_t *>(w == 0 ? p.scales[GLU ? i >> 1 : 0]
+                                                                                : p.biases[GLU ? i >> 1 : 0]) + from;
+                        const uint32_t d = win + w * win_bytes + i * 1024;
+                        const int64_t left = p.bytes_sb - from;
+                        if (left > 0) cp_async16(d, src, (uint32_t)min(left, (int64_t)16));
+                        if (left > 16) cp_async16(d + 16, src + 16, (uint32_t)min(left - 16, (int64_t)16));
                     }
                 }
-                if (p.sb_vec == 2) ptx::mbar_arrive(full_p + 8 * ps.slot);
-                else cp_async_arrive(full_p + 8 * ps.slot);
+                cp_async_arrive(full_p + 8 * ps.slot);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -938,6 +941,19 @@ cudaError_t launch_chained(dim3 grid, int threads, size_t smem, cudaStream_t s, 
 // there are few of them, and the rings hold more packed stages then.
 int chunk_cap(int64_t slots, int64_t E) { return slots <= 32 * E ? 64 : kMaxCap; }
 
+constexpr size_t kSmemMax = 227 * 1024;
+
+template <typename T, int MODE, bool GLU, int CAP, int WIN>
+cudaError_t launch_product(int grid, size_t smem, cudaStream_t s, const WeightMaps &mw, const ActMaps &mb, const TcParams &p) {
+    auto kern = moe_tc_kernel<T, MODE, GLU, CAP, WIN>;
+    struct Tag;
+    const cudaError_t e = configure_once<Tag>(kSmemMax, [&]() {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_chained<moe_tc_kernel<T, MODE, GLU, CAP, WIN>>(dim3(grid), kThreads, smem, s, mw, mb, p);
+}
+
 template <typename T, int MODE, bool GLU, int CAP>
 cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) {
     using Cfg = TileCfg<CAP>;
@@ -948,7 +964,8 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) 
     const ExpertWeight *ew[2] = {GLU ? &a.gate : &a.down, GLU ? &a.up : &a.down};
     TcParams p{};
     p.row_bytes_sb = C / a.group_size * ES;
-    p.sb_vec = p.row_bytes_sb % 16 == 0 ? 16 : (p.row_bytes_sb % 4 == 0 ? 4 : 2);
+    p.win = p.row_bytes_sb % 16 == 0 ? 16 : 32;
+    p.bytes_sb = a.n_experts * R * p.row_bytes_sb;
     WeightMaps mw{};
     const uint64_t rows = (uint64_t)(a.n_experts * R);
     const CUtensorMapDataType st = ES == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -960,7 +977,7 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) 
         if (!make_map_2d(&mw.w[m], CU_TENSOR_MAP_DATA_TYPE_UINT32, ew[m]->wq, (uint64_t)C / 8, rows, (uint64_t)C / 2,
                          kStageK / 8, kBM / NM, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
-        if (p.sb_vec == 16 &&
+        if (p.win == 16 &&
             (!window(&mw.s[m], ew[m]->scales) || (NW == 2 && !window(&mw.b[m], ew[m]->biases))))
             return cudaErrorInvalidValue;
     }
@@ -985,9 +1002,8 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) 
     p.KB = (int)(C / kBK);
     p.gs_log = a.group_size == 16 ? 4 : (a.group_size == 32 ? 5 : (a.group_size == 64 ? 6 : 7));
     p.n_tiles = (int)((R + kBM / NM - 1) / (kBM / NM));
-    constexpr size_t kSmemMax = 227 * 1024;
     const size_t fixed = 1024 + kBarBytes;  // alignment; barriers
-    const size_t p_bytes = kPBytes + NW * kWinBytes;
+    const size_t p_bytes = kPBytes + NW * kBM * p.win;
     p.SP = (int)std::min<size_t>(8, (kSmemMax - fixed - (size_t)Cfg::SB * Cfg::BBytes) / p_bytes);
     if (p.SP < 2) return cudaErrorInvalidConfiguration;
     const size_t smem = fixed + (size_t)Cfg::SB * Cfg::BBytes + p.SP * p_bytes;
@@ -995,15 +1011,10 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) 
     p.hdr = reinterpret_cast<const MoeHeader *>(ws + w.hdr);
     p.chunks = reinterpret_cast<const int4 *>(ws + w.chunks);
     p.err = device_error_word();
-    auto kern = moe_tc_kernel<T, MODE, GLU, CAP>;
-    struct Tag;
-    cudaError_t e = configure_once<Tag>(kSmemMax, [&]() {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
-    });
-    if (e != cudaSuccess) return e;
     const int64_t most = std::min<int64_t>(w.max_chunks, std::min<int64_t>(P, a.n_experts) + P / 16) * p.n_tiles;
     const int grid = (int)std::min<int64_t>(std::max<int64_t>(most, 1), num_sms());
-    return launch_chained<moe_tc_kernel<T, MODE, GLU, CAP>>(dim3(grid), kThreads, smem, s, mw, mb, p);
+    return p.win == 16 ? launch_product<T, MODE, GLU, CAP, 16>(grid, smem, s, mw, mb, p)
+                       : launch_product<T, MODE, GLU, CAP, 32>(grid, smem, s, mw, mb, p);
 }
 
 template <typename T, int MODE>

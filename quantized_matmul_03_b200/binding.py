@@ -541,19 +541,19 @@ def qmm_moe_experts(x, indices, weights, gate, up, down, group_size: int = 64, b
     T = x.numel() // K if K else 0
     if slots != weights.shape or indices.numel() != T * top_k:
         raise ValueError(f"indices and weights must be [{T}, top_k]")
-    for w in (gate, up, down):
-        if w[0].dim() != 3 or w[0].dtype != torch.int32 or w[1].dim() != 3:
-            raise ValueError("expert weights are stacked [n_experts, rows, words] int32 with scales [n_experts, rows, groups]")
-    n_experts, I, _ = gate[0].shape
-    N = down[0].shape[1]
+    gs, ds = gate[0].shape, down[0].shape
+    if len(gs) != 3 or len(ds) != 3:
+        raise ValueError("expert weights are stacked [n_experts, rows, words] int32 with scales [n_experts, rows, groups]")
+    n_experts, I, N = gs[0], gs[1], ds[1]
     if mode not in MX_MODES and mode != "affine":
         raise ValueError(f"unknown mode {mode}")
     sdt = torch.uint8 if mode in MX_MODES else x.dtype
     for name, w, rows, cols in (("gate", gate, I, K), ("up", up, I, K), ("down", down, N, I)):
-        if w[0].shape != (n_experts, rows, cols * bits // 32):
-            raise ValueError(f"{name}: packed weight must be {(n_experts, rows, cols * bits // 32)}")
+        wq, scales, biases = w
+        if wq.shape != (n_experts, rows, cols * bits // 32) or wq.dtype != torch.int32:
+            raise ValueError(f"{name}: packed weight must be {(n_experts, rows, cols * bits // 32)} int32")
         groups = (n_experts, rows, cols // group_size)
-        for s in w[1:]:
+        for s in (scales, biases):
             if s is not None and (s.shape != groups or s.dtype != sdt):
                 raise ValueError(f"{name}: scales and biases must be {groups} {sdt}")
     if out is None:
@@ -565,7 +565,7 @@ def qmm_moe_experts(x, indices, weights, gate, up, down, group_size: int = 64, b
             workspace = torch.empty(qmm_moe_experts_workspace_size(T, K, top_k, n_experts, I, N, x.dtype),
                                     dtype=torch.uint8, device=x.device)
         _check(lib().qmm_moe_experts(_p(x), T, K, _dtype(x), _p(indices), _p(weights), top_k,
-                                     *map(_p, gate), *map(_p, up), *map(_p, down), n_experts, I, N,
+                                     *[t if t is None else t.data_ptr() for t in (*gate, *up, *down)], n_experts, I, N,
                                      group_size, bits, _mode(mode), ACTIVATIONS[activation], _p(out),
                                      _p(workspace), workspace.numel() * workspace.element_size(),
                                      _stream(x.device)))

@@ -158,17 +158,19 @@ __device__ __forceinline__ void scores_of(const float (&l)[V], int lane, int E, 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             // The largest logit's term is 1 also where it is infinite; a token
-            // whose logits are all -inf has no terms.
-            if (m == __uint_as_float(0xff800000u)) s[i] = 0;
+            // whose logits are all -inf has no terms.  A NaN logit has a NaN
+            // score and is left out of the sum, as out of the maximum, so that
+            // the others keep their order.
+            if (m == __uint_as_float(0xff800000u)) s[i] = l[i] == l[i] ? F(0) : F(l[i]);
             else if (l[i] == m) s[i] = 1;
             else if constexpr (std::is_same<F, double>::value) s[i] = exp((double)l[i] - (double)m);
             else s[i] = __expf(l[i] - m);
-            if (lane * V + i < E) z += s[i];
+            if (lane * V + i < E && s[i] == s[i]) z += s[i];
         }
         z = warp_sum(z);
-        const F inv = z > 0 ? F(1) / z : z;  // NaN stays NaN
+        const F inv = z > 0 ? F(1) / z : F(0);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = std::is_same<F, double>::value ? (z > 0 ? s[i] / z : z) : s[i] * inv;
+        for (int i = 0; i < V; ++i) s[i] = std::is_same<F, double>::value && z > 0 ? s[i] / z : s[i] * inv;
     }
 }
 

@@ -424,10 +424,11 @@ qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t T, int64_t
  *   preserved.  Two calls in flight at once must not share a workspace (two
  *   captured graphs that may run at once need one each).  Too small or
  *   misaligned: QMM_ERR_WORKSPACE.
- * Limits: K and I multiples of 64 and of group_size, QMM_ERR_UNSUPPORTED for
- *   other sizes of K and I, other bits or modes, QMM_F32, and more than 2^30
- *   slots or stacked rows; n_experts <= 1024, top_k <= 32.  T == 0 or N == 0
- *   is a no-op.  QMM_PATH_GEMV takes top_k * max(K, I) up to 2^23 * 3 / 2 (K or I
+ * Limits: K and I multiples of 64 and of group_size, at most 2^24;
+ *   QMM_ERR_UNSUPPORTED for other sizes of K and I, other bits or modes,
+ *   QMM_F32, and more than 2^30 slots or stacked rows (T * top_k, n_experts * I,
+ *   n_experts * N); n_experts <= 1024, top_k <= 32.  The workspace size is 0
+ *   beyond these limits.  T == 0 or N == 0 is a no-op.  QMM_PATH_GEMV takes top_k * max(K, I) up to 2^23 * 3 / 2 (K or I
  *   rounded up to 1024) and returns QMM_ERR_UNSUPPORTED beyond.
  */
 typedef enum { QMM_ACT_SILU = 0, QMM_ACT_GELU_TANH = 1 } qmm_activation;

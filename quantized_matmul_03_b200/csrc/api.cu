@@ -141,6 +141,13 @@ bool moe_few_rows(const ExpertsArgs &a) {
     return moe_gemv_supported(a) && slots <= 40 && (slots - touched) * (double)a.I * (2.0 * a.K + a.N) <= 6e7;
 }
 
+// Sizes of qmm_moe_experts within the kernels' index ranges (positive
+// n_experts and top_k); the workspace has a size for exactly these.
+bool moe_experts_sizes(int64_t T, int64_t K, int64_t top_k, int64_t n_experts, int64_t I, int64_t N) {
+    return T <= (1 << 30) / top_k && K <= (1 << 24) && I <= (1 << 24) && I <= (1 << 30) / n_experts &&
+           N <= (1 << 30) / n_experts;
+}
+
 qmm_status finish_launch(cudaError_t e, const char *what) {
     if (e != cudaSuccess) return cuda_fail(e, what);
     return QMM_OK;
@@ -713,7 +720,7 @@ size_t qmm_moe_experts_workspace_size(int64_t T, int64_t K, int64_t top_k, int64
                                       int64_t N, qmm_dtype dtype) {
     if (T <= 0 || K <= 0 || I <= 0 || N <= 0 || top_k < 1 || top_k > kMoeMaxTopK) return 0;
     if (n_experts < 1 || n_experts > kMoeMaxExperts || (dtype != QMM_BF16 && dtype != QMM_F16)) return 0;
-    if (T > (1 << 30) / top_k || K > (1 << 24) || I > (1 << 24) || N > (1 << 24)) return 0;
+    if (!moe_experts_sizes(T, K, top_k, n_experts, I, N)) return 0;
     ExpertsArgs a{};
     a.T = T;
     a.K = K;
@@ -750,9 +757,8 @@ qmm_status qmm_moe_experts(const void *x, int64_t T, int64_t K, qmm_dtype dtype,
             return fail(QMM_ERR_UNSUPPORTED,
                         "the experts' product takes 4-bit weights, bf16/f16 activations, and K and I in "
                         "multiples of 64");
-        if (T > (1 << 30) / top_k || K > (1 << 24) || I > (1 << 24) || n_experts * I > (1 << 30) ||
-            n_experts * N > (1 << 30))
-            return fail(QMM_ERR_UNSUPPORTED, "sizes beyond 2^30 slots or stacked rows");
+        if (!moe_experts_sizes(T, K, top_k, n_experts, I, N))
+            return fail(QMM_ERR_UNSUPPORTED, "sizes beyond 2^30 slots or stacked rows, or K or I beyond 2^24");
         if (T == 0 || N == 0) return QMM_OK;
         QMM_CHECK_PTR(x, "x");
         QMM_CHECK_PTR(y, "y");

@@ -942,9 +942,24 @@ cudaError_t launch_chained(dim3 grid, int threads, size_t smem, cudaStream_t s, 
 int chunk_cap(int64_t slots, int64_t E) { return slots <= 32 * E ? 64 : kMaxCap; }
 
 constexpr size_t kSmemMax = 227 * 1024;
+constexpr size_t kSmemFixed = 1024 + kBarBytes;  // alignment; barriers
+
+// Packed stages that fit beside the activations, p_bytes each with their windows.
+template <int CAP>
+constexpr int packed_stages(size_t p_bytes) {
+    return (int)std::min<size_t>(8, (kSmemMax - kSmemFixed - (size_t)TileCfg<CAP>::SB * TileCfg<CAP>::BBytes) / p_bytes);
+}
 
 template <typename T, int MODE, bool GLU, int CAP, int WIN>
 cudaError_t launch_product(int grid, size_t smem, cudaStream_t s, const WeightMaps &mw, const ActMaps &mb, const TcParams &p) {
+    // A group that visits every BPG-th stage waits for the parity of stage s in
+    // a ring slot whose last stage, s - SP, it did not take itself: were that one
+    // still on its way, the wait would pass on the phase before it.  The group's
+    // stage before, s - BPG, waited for the MMAs of unit s - BPG - NU (a unit is a
+    // stage here), so that stages up to that one have arrived.
+    using Cfg = TileCfg<CAP>;
+    constexpr int SP = packed_stages<CAP>(kPBytes + (MODE == QMM_MODE_AFFINE ? 2 : 1) * kBM * WIN);
+    static_assert(SP >= 2 && (Cfg::BPG == 1 || (Cfg::U == kGroups && SP >= Cfg::NU + Cfg::BPG)), "packed ring too short");
     auto kern = moe_tc_kernel<T, MODE, GLU, CAP, WIN>;
     struct Tag;
     const cudaError_t e = configure_once<Tag>(kSmemMax, [&]() {
@@ -1002,11 +1017,9 @@ cudaError_t run_product(const ExpertsArgs &a, const MoePlan &w, cudaStream_t s) 
     p.KB = (int)(C / kBK);
     p.gs_log = a.group_size == 16 ? 4 : (a.group_size == 32 ? 5 : (a.group_size == 64 ? 6 : 7));
     p.n_tiles = (int)((R + kBM / NM - 1) / (kBM / NM));
-    const size_t fixed = 1024 + kBarBytes;  // alignment; barriers
     const size_t p_bytes = kPBytes + NW * kBM * p.win;
-    p.SP = (int)std::min<size_t>(8, (kSmemMax - fixed - (size_t)Cfg::SB * Cfg::BBytes) / p_bytes);
-    if (p.SP < 2) return cudaErrorInvalidConfiguration;
-    const size_t smem = fixed + (size_t)Cfg::SB * Cfg::BBytes + p.SP * p_bytes;
+    p.SP = packed_stages<CAP>(p_bytes);
+    const size_t smem = kSmemFixed + (size_t)Cfg::SB * Cfg::BBytes + p.SP * p_bytes;
     p.act = a.act;
     p.hdr = reinterpret_cast<const MoeHeader *>(ws + w.hdr);
     p.chunks = reinterpret_cast<const int4 *>(ws + w.chunks);

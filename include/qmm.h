@@ -380,11 +380,14 @@ qmm_status qmm_gather_qmm_static(const void *x, int64_t x_batch, int64_t M, int6
  *   for no groups.
  * Weights: the chosen experts' s (no bias), divided by their sum if
  *   renormalize, times scale (finite).
- * Masked experts: a logit of -inf (score 0) or a bias of -inf ranks below every
- *   finite key.  A token whose logits are all -inf has scores 0: it gets the
- *   lowest indices and weights 0, and so do chosen experts whose sum is 0.
- *   Softmax of logits that hold +inf is shared by those.  A NaN logit ranks
- *   below everything and makes the token's weights NaN.
+ * Masked experts: a logit of -inf has score 0, and without a bias its key lies
+ *   below every finite one.  With a bias its key is the bias alone, which may
+ *   win: mask such an expert by a bias of -inf, below every finite key too.  A
+ *   token whose logits are all -inf has scores 0: without a bias it gets the
+ *   lowest indices and weights 0, and weights 0 also have chosen experts whose
+ *   sum is 0.  Softmax of logits that hold +inf is shared by those.  A NaN logit
+ *   ranks below everything, leaves the other experts' scores as they are, and
+ *   makes the token's weights NaN.
  * Limits: 1 <= E <= 1024, 1 <= top_k <= min(32, topk_groups * E / n_groups).
  *   T == 0 is a no-op.
  */
@@ -414,10 +417,12 @@ qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t T, int64_t
  *   twice for one token; both slots count.
  * Rounding: sums are fp32 or exact integers, and y is rounded once.  With few
  *   rows (and under QMM_PATH_GEMV) activations enter as 16-bit integers per 32
- *   elements (error at most 2^-14 of their largest) and h stays fp32; with more
- *   rows (and under QMM_PATH_GEMM) h is rounded to `dtype`, the tensor cores'
- *   operand, and so is each weight of the "affine" mode and of "nvfp4" and
- *   "mxfp4" where X * element is no `dtype` value (never for normal ones).
+ *   elements (error at most 2^-14 of their largest, or 2^-127) and h stays fp32;
+ *   with more rows (and under QMM_PATH_GEMM) h is rounded to `dtype`, the tensor
+ *   cores' operand, and so is each weight of the "affine" mode and of "nvfp4" and
+ *   "mxfp4" where X * element is no `dtype` value (never for normal ones).  In
+ *   QMM_F16 that rounding is to infinity where h or a weight passes 65504: such a
+ *   token can be finite among few rows and infinite or NaN among many.
  *   A slot's result is added in slot order: repeated calls return the same bits.
  * workspace: device memory of qmm_moe_experts_workspace_size(...) bytes,
  *   256-byte aligned; its contents need not be initialised and are not

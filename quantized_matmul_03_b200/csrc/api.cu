@@ -131,10 +131,15 @@ bool gather_tc_supported(qmm_dtype dtype, int64_t x_batch, int64_t M, int64_t K,
 // rate (5 to 6e12 weights a second), and the latter costs about 12 us more per
 // call (sort, combine, tiles that are mostly empty): few rows while the slots
 // beyond the number of experts they are expected to touch cost less than that.
-// Measured, few-row / tensor-core path: 2 and 4 slots over 8 experts 4096 x
-// 14336 67 / 101 and 132 / 114 us; 8 and 12 slots over 16 experts 2048 x 2048
-// 34 / 42 and 46 / 43; 32 and 48 slots over 64 experts 2048 x 1024 50 / 54 and
-// 71 / 63, 1024 x 512 28 / 32 and 36 / 32.
+// Measured, single calls with cold caches, few-row / tensor-core path in us: 2
+// and 4 slots over 8 experts 4096 x 14336, mxfp4 65 / 102 and 124 / 115, nvfp4
+// 71 / 110 and 124 / 126, affine 58 / 94 and 114 / 106; 8, 12 and 16 slots over 16
+// experts 2048 x 2048, affine 34 / 38, 46 / 40 and 54 / 42, nvfp4 32 / 42, 44 / 44
+// and 52 / 46; 32, 40 and 48 slots over 64 experts 2048 x 1024 mxfp4 52 / 52,
+// 61 / 58 and 71 / 59, 1024 x 512 28 / 32, 32 / 33 and 36 / 34; with rows of
+// scales that the ring does not take, 12 and 24 slots over 32 experts 2880 x 2880
+// mxfp4 69 / 80 and 112 / 112, 18 and 36 over 64 experts 2048 x 1408 affine
+// 58 / 54 and 95 / 77.
 bool moe_few_rows(const ExpertsArgs &a) {
     const double slots = (double)a.T * a.top_k, E = (double)a.n_experts;
     const double touched = E * (1.0 - std::pow(1.0 - 1.0 / E, slots));

@@ -11,19 +11,21 @@
 // token's slots there, weighted, and rounds once.
 //
 // Arithmetic.  32 activations are held as 16-bit integers over a common power
-// of two (error at most 2^-14 of the largest of the 32), codes are small
-// integers, and DP2A sums their products exactly: 4-bit affine codes as they
-// are, E2M1 codes doubled (an integer in [-12, 12]) and offset by 64, which
-// -64 sum(x_int) takes out again.  The integer sum is scaled by the group's
+// of two (error at most 2^-14 of the largest of the 32, or 2^-127: finer than the
+// rounding of that one to a 16-bit type; DP2A takes two of them per instruction),
+// codes are small integers, and DP2A sums their products exactly: 4-bit affine
+// codes as they are, E2M1 codes doubled (an integer in [-12, 12]) and offset by 64,
+// which -64 sum(x_int) takes out again.  The integer sum is scaled by the group's
 // scale in fp32.  Between the kernels h stays in fp32.
 //
 // Every code is read once per slot.  Two forms of each kernel: weights streamed
 // through shared memory by bulk copies (moe_stream_kernel), and, for shapes that
 // those cannot take, loaded 16 bytes per lane with two batches of eight loads in
 // flight per warp (moe_gemv_kernel).  One token, 2 of 8 experts 4096 x 14336
-// mxfp4, 187 MB: 56 us (3.3 TB/s; 69 us with plain loads); 8 of 64 experts 2048
-// x 1024 nvfp4, 28 MB: 22 us.  Bound: the two launches with their ring's first
-// and last stages, and between them the consumer warps' instructions.
+// mxfp4, 187 MB: 56 us per call back to back (3.3 TB/s; 69 us with plain loads),
+// a single cold call 65 us; 8 of 64 experts 2048 x 1024 nvfp4, 28 MB: 24 us cold.
+// Bound: the two launches with their ring's first and last stages, and between
+// them the consumer warps' instructions.
 #include "moe.cuh"
 #include "mx.cuh"
 #include "ptx_sm100.cuh"
@@ -119,8 +121,8 @@ __device__ __forceinline__ uint32_t mad(uint32_t a, uint32_t b, uint32_t c) {
 // non-negative code and 0 for a negative one (selector bit 3 asks for the sign
 // of a table byte), of the second by the nibbles with their sign bits flipped
 // the converse.  The integer pipe is the kernel's busiest: their sum goes to the
-// multiply pipe (one token, 2 of 8 experts 4096 x 14336: 63 us, 65.5 with
-// integer additions).
+// multiply pipe (one token, 2 of 8 experts 4096 x 14336, single cold calls: 63 us,
+// 65.5 with integer additions).
 __device__ __forceinline__ void e2m1_bytes(const E2m1Table &t, uint32_t w, uint32_t &lo, uint32_t &hi) {
     const uint32_t n = w ^ 0x88888888u;
     lo = mad(prmt(t.pa, t.pb, w), t.one, prmt(t.na, t.nb, n));

@@ -425,7 +425,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 4 : 2) moe_route_ke
         }
         if (q == i0) my_nan = nan;
         if (SCORE == QMM_SCORE_SOFTMAX && !p.renormalize) {
-            // the largest logit and the sum over all experts relative to it
+            // The largest logit and the sum over all experts relative to it: terms
+            // and a lane's V additions in fp32, at most V + 8 units of 2^-24 off
+            // (expf 2, its argument ln E in the mean), the 32 lanes in fp64.
             float m = l[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);

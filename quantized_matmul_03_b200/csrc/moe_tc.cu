@@ -49,13 +49,20 @@
 // kHeights), and k-blocks reach the MMA thread in units of 4 (of 2 with tall
 // chunks, whose accumulators leave less tensor memory).
 //
+// Rounding.  The MMA's operands are 16 bits: h is rounded to the activations'
+// type, and so is an affine weight s q + b; E2M1 weights are exact while X times
+// the element is a normal value.  (Two 16-bit pieces per value would keep them,
+// at twice the MMAs and twice the tensor memory; the library's GEMM rounds
+// weights alike.)  The accumulators, and the rows that the combine adds, are fp32.
+//
 // Bound: with few rows per expert the dequantize warps' instructions (about 3
 // per element), with many rows the tensor cores and, on short contractions, the
-// epilogue.  2048 rows, 8 experts 4096 x 14336, 2 each, nvfp4: gate/up 645 us,
-// down 416 us (1.36e15 operations a second); 512 rows: 230 and 165 us.  Two CTAs
-// sharing an activation tile (MMAs of 256 rows) measured 741 and 446, 292 and
-// 200 us where one measured 777 and 465, 273 and 191: the hand-overs between the
-// two cost what the halved copies save.
+// epilogue.  Single cold calls: 2048 rows, 8 experts 4096 x 14336, 2 each, nvfp4:
+// gate/up 645 us, down 416 us (1.36e15 operations a second; back to back, at the
+// power limit, the whole call takes 1293 us, 1.1e15); 512 rows: 230 and 165 us.
+// Two CTAs sharing an activation tile (MMAs of 256 rows) measured 741 and 446, 292
+// and 200 us where one measured 777 and 465, 273 and 191: the hand-overs between
+// the two cost what the halved copies save.
 #include <cuda.h>
 
 #include <algorithm>
@@ -304,7 +311,9 @@ __device__ __forceinline__ void dequant_block(const uint32_t (&w)[8], uint32_t s
     }
 }
 
-// Gated activation for a value that is rounded to 16 bits next.
+// Gated activation for a value that is rounded to 16 bits next: the fast
+// exponential and division stay within 2^-16 of the value (2 + 1.2 |z| units of
+// 2^-23, |z| < 88), below that rounding.
 template <int ACT>
 __device__ __forceinline__ float gate_fast(float g) {
     float z = g;
@@ -748,12 +757,14 @@ __device__ __forceinline__ int box_of(int rows) {
 
 // Each CTA counts every slot's expert for itself (the indices are small and
 // come from L2; 32768 slots of 64 experts, copied rows of 4 KB: 39 us for the
-// kernel, 90 with lanes of the same expert matched before they add), which gives
-// it, without a second kernel, where the slots of its own stretch go: the experts' first rows, plus the same expert's slots in
-// earlier stretches, plus the rank within its own.  It then copies their rows
-// of x there, every eight elements in the order 0 4 1 5 2 6 3 7.  The first CTA also cuts each expert's rows into near-equal
-// chunks of whole 16 rows, at most cap.  Counts are integers, and ranks follow
-// the slots' order, so the result does not depend on timing.
+// kernel, 90 with lanes of the same expert matched before they add).  That gives
+// it, without a second kernel, where the slots of its own stretch go: the
+// experts' first rows, plus the same expert's slots in earlier stretches, plus
+// the rank within its own.  It then copies their rows of x there, every eight
+// elements in the order 0 4 1 5 2 6 3 7.  The first CTA also cuts each expert's
+// rows into near-equal chunks of whole 16 rows, at most cap.  Counts are
+// integers, and ranks follow the slots' order, so the result does not depend on
+// timing.
 __global__ void __launch_bounds__(kPrepThreads) moe_prep_kernel(const PrepParams p) {
     extern __shared__ int sm[];
     __shared__ int tmp[kPrepWarps];
